@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes as C
 import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -30,6 +31,14 @@ LLMINT8_ERR_HIP = 5
 LLMINT8_MAX_K = 133144
 LLMINT8_NOALLOC_SCRATCH_BYTES = 32 << 20
 
+LLMINT8_FP16 = 0
+LLMINT8_BF16 = 1
+LLMINT8_ACT_NONE = 0
+LLMINT8_ACT_RELU = 1
+LLMINT8_ACT_GELU = 2
+LLMINT8_ACT_GELU_TANH = 3
+LLMINT8_ACT_SILU = 4
+
 _lib = None
 
 
@@ -46,6 +55,19 @@ class LinearOpts(C.Structure):
 
     def __init__(self, **kw):
         super().__init__(struct_size=C.sizeof(LinearOpts), **kw)
+
+
+class SavedMatrix(C.Structure):
+    """Mirror of llmint8_saved."""
+    _fields_ = [("data", C.c_void_p), ("ld", C.c_int64), ("scales", C.c_void_p),
+                ("ld_scales", C.c_int64)]
+
+
+class MatmulOpts(C.Structure):
+    """Mirror of llmint8_matmul_opts."""
+    _fields_ = [("struct_size", C.c_size_t), ("activation", C.c_int), ("bias", C.c_void_p),
+                ("residual", C.c_void_p), ("ldr", C.c_int64), ("Z", C.c_void_p),
+                ("ldz", C.c_int64)]
 
 
 class Llmint8Error(RuntimeError):
@@ -92,6 +114,18 @@ def lib() -> C.CDLL:
         L.llmint8_linear_fp8_workspace_size.argtypes = [i64, i64, i64]
         L.llmint8_linear_fp8_workspace_size.restype = sz
         L.llmint8_linear_fp8.argtypes = L.llmint8_linear_ex.argtypes
+        i = C.c_int
+        L.llmint8_checkpoint_pack.argtypes = [p, i64, i64, i64, i, p, p]
+        L.llmint8_checkpoint_unpack.argtypes = [p, i64, i64, i, p, i64, p]
+        L.llmint8_matmul.argtypes = [p, i64, i64, i64, p, i64, i64, i, p, i64, p, p, sz, p]
+        L.llmint8_matmul_backward.argtypes = [p, i64, i64, i64, p, i64, p, i64, p, i64, i, i, p,
+                                              i64, p, i64, p, p, sz, p]
+        L.llmint8_gated.argtypes = [p, i64, i64, i64, p, p, i64, i64, i, i, p, i64, p, p, p, sz, p]
+        L.llmint8_gated_backward.argtypes = [p, i64, i64, i64, p, i64, p, p, i64, p, p, i, i, p,
+                                             i64, p, p, i64, p, sz, p]
+        for name in ("matmul", "matmul_backward", "gated", "gated_backward"):
+            query = getattr(L, f"llmint8_{name}_workspace_size")
+            query.argtypes, query.restype = [i64, i64, i64], sz
         L.llmint8_status_string.argtypes = [C.c_int]
         L.llmint8_status_string.restype = C.c_char_p
         for name in ("llmint8_quantize_colwise", "llmint8_find_outliers",
@@ -99,7 +133,9 @@ def lib() -> C.CDLL:
                      "llmint8_linear_noalloc",
                      "llmint8_quantize_tensorwise", "llmint8_linear_tensorwise",
                      "llmint8_quantize_colwise_fp8", "llmint8_quantize_rowwise_fp8",
-                     "llmint8_linear_fp8"):
+                     "llmint8_linear_fp8", "llmint8_checkpoint_pack",
+                     "llmint8_checkpoint_unpack", "llmint8_matmul", "llmint8_matmul_backward",
+                     "llmint8_gated", "llmint8_gated_backward"):
             getattr(L, name).restype = C.c_int
         _lib = L
     return _lib
@@ -472,3 +508,296 @@ def llmint8_linear_fp8(X: torch.Tensor, Wq8: torch.Tensor, col_absmax: torch.Ten
         _ptr(outlier_count), _ptr(C_debug), *_ws(workspace), _stream(X),
         C.byref(o)))
     return Y
+
+
+# ---- 16-bit feed-forward operators ---------------------------------------------------
+
+_DTYPES = {torch.float16: LLMINT8_FP16, torch.bfloat16: LLMINT8_BF16}
+_ACTIVATIONS = {"none": LLMINT8_ACT_NONE, "relu": LLMINT8_ACT_RELU, "gelu": LLMINT8_ACT_GELU,
+                "gelu_tanh": LLMINT8_ACT_GELU_TANH, "silu": LLMINT8_ACT_SILU}
+CHECKPOINT_BLOCK = 32
+
+
+class Checkpoint(NamedTuple):
+    """An 8-bit activation checkpoint: int8 codes [M, K] (row pitch a multiple of 16) and
+    the scale bytes [M, ceil(K / 32)]; an entry stands for code * 2^(byte - 127)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def _dtype_of(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _activation(name: str) -> int:
+    if name not in _ACTIVATIONS:
+        raise ValueError(f"activation is one of {sorted(_ACTIVATIONS)}, got {name!r}")
+    return _ACTIVATIONS[name]
+
+
+def _matrix(t, name: str, like: torch.Tensor, shape=None) -> int:
+    """The leading dimension of a matrix of like's dtype and device."""
+    _need(t, name, like.dtype, 2)
+    if shape is not None:
+        _need_shape(t, name, shape)
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    return _ld(t, name)
+
+
+def _out(t, name: str, like: torch.Tensor, shape) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    _matrix(t, name, like, shape)
+    return t
+
+
+def _new_checkpoint(M: int, K: int, device) -> Checkpoint:
+    codes = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :K]
+    return Checkpoint(codes, torch.empty((M, -(-K // CHECKPOINT_BLOCK)), dtype=torch.uint8,
+                                         device=device))
+
+
+def _checkpoint(c, name: str, device, shape=None) -> SavedMatrix:
+    """The C view of a checkpoint, after checking it."""
+    codes, scales = c
+    _need(codes, f"{name}.codes", torch.int8, 2)
+    if shape is not None:
+        _need_shape(codes, f"{name}.codes", shape)
+    M, K = codes.shape
+    _need(scales, f"{name}.scales", torch.uint8, 2)
+    _need_shape(scales, f"{name}.scales", (M, -(-K // CHECKPOINT_BLOCK)))
+    if codes.device != device or scales.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    pad = (K + 15) // 16 * 16
+    ld = codes.stride(0) if M > 1 else pad
+    if (K > 1 and codes.stride(1) != 1) or ld < pad:
+        raise ValueError(f"{name}.codes must have unit stride and rows padded to 16 entries")
+    # the calls read each row of codes to the next multiple of 16
+    held = codes.untyped_storage().nbytes() - codes.storage_offset()
+    if held < (M - 1) * ld + pad:
+        raise ValueError(f"{name}.codes: the last row must be padded to 16 entries")
+    return SavedMatrix(codes.data_ptr(), ld, scales.data_ptr(), _ld(scales, f"{name}.scales"))
+
+
+def _saved(t, name: str, like: torch.Tensor, shape) -> SavedMatrix:
+    """The C view of a matrix held in 16 bits or as a checkpoint."""
+    if isinstance(t, tuple):
+        return _checkpoint(t, name, like.device, shape)
+    return SavedMatrix(t.data_ptr() if isinstance(t, torch.Tensor) else None,
+                       _matrix(t, name, like, shape), None, 0)
+
+
+def _workspace(workspace, need: int, device):
+    """(pointer, size) of the caller's workspace, or of one allocated here."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
+    return _ws(workspace)
+
+
+def llmint8_checkpoint_pack(X: torch.Tensor) -> Checkpoint:
+    """fp16 or bf16 X [M, K] -> its 8-bit checkpoint."""
+    dt = _dtype_of(X, "X")
+    ldx = _matrix(X, "X", X)
+    M, K = X.shape
+    c = _new_checkpoint(M, K, X.device)
+    out = _checkpoint(c, "checkpoint", X.device)
+    _check(lib().llmint8_checkpoint_pack(_ptr(X), M, K, ldx, dt, C.byref(out), _stream(X)))
+    return c
+
+
+def llmint8_checkpoint_unpack(checkpoint: Checkpoint, dtype=torch.float16, *,
+                              X=None) -> torch.Tensor:
+    """What a checkpoint stands for, as a 16-bit matrix [M, K] of `dtype`."""
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
+    codes = checkpoint[0]
+    _need(codes, "checkpoint.codes", torch.int8, 2)
+    saved = _checkpoint(checkpoint, "checkpoint", codes.device)
+    M, K = codes.shape
+    like = torch.empty((0,), dtype=dtype, device=codes.device) if X is not None else None
+    X = (torch.empty((M, K), dtype=dtype, device=codes.device) if X is None
+         else _out(X, "X", like, (M, K)))
+    _check(lib().llmint8_checkpoint_unpack(C.byref(saved), M, K, _DTYPES[dtype], _ptr(X),
+                                           _ld(X, "X"), _stream(X)))
+    return X
+
+
+def llmint8_matmul_workspace_size(M: int, K: int, N: int) -> int:
+    return int(lib().llmint8_matmul_workspace_size(M, K, N))
+
+
+def llmint8_matmul(X: torch.Tensor, W: torch.Tensor, *, bias: torch.Tensor | None = None,
+                   activation: str = "none", residual: torch.Tensor | None = None,
+                   Y=None, Z=None, workspace=None) -> torch.Tensor:
+    """Y = act(X W + bias) + residual in one product: fp16 or bf16 X [M, K], W [K, N],
+    bias [N] and residual [M, N] of the same dtype -> Y [M, N].
+
+    activation is "none", "relu", "gelu", "gelu_tanh" or "silu". Z, if given, receives the
+    pre-activations X W + bias [M, N] that llmint8_matmul_backward takes."""
+    dt = _dtype_of(X, "X")
+    ldx = _matrix(X, "X", X)
+    M, K = X.shape
+    ldw = _matrix(W, "W", X)
+    N = W.shape[1]
+    if W.shape[0] != K:
+        raise ValueError(f"W must be [{K}, N], got {tuple(W.shape)}")
+    Y = _out(Y, "Y", X, (M, N))
+    act = _activation(activation)
+    opts = None
+    if act or bias is not None or residual is not None or Z is not None:
+        opts = MatmulOpts(struct_size=C.sizeof(MatmulOpts), activation=act)
+        if bias is not None:
+            _need_vec(bias, "bias", X.dtype, N)
+            opts.bias = bias.data_ptr()
+        if residual is not None:
+            opts.ldr = _matrix(residual, "residual", X, (M, N))
+            opts.residual = residual.data_ptr()
+        if Z is not None:
+            opts.ldz = _matrix(Z, "Z", X, (M, N))
+            opts.Z = Z.data_ptr()
+    L = lib()
+    ws, nb = _workspace(workspace, L.llmint8_matmul_workspace_size(M, K, N), X.device)
+    _check(L.llmint8_matmul(_ptr(X), M, K, ldx, _ptr(W), ldw, N, dt, _ptr(Y), _ld(Y, "Y"),
+                            C.byref(opts) if opts is not None else None, ws, nb, _stream(X)))
+    return Y
+
+
+def llmint8_matmul_backward_workspace_size(M: int, K: int, N: int) -> int:
+    return int(lib().llmint8_matmul_backward_workspace_size(M, K, N))
+
+
+def llmint8_matmul_backward(dY: torch.Tensor, X, W: torch.Tensor | None, *,
+                            Z: torch.Tensor | None = None, activation: str = "none",
+                            need_dX: bool = True, need_dW: bool = True, need_dbias: bool = False,
+                            dX=None, dW=None, dbias=None, workspace=None):
+    """Gradients of llmint8_matmul from dY [M, N]: (dX [M, K], dW [K, N], dbias fp32 [N]),
+    None where not needed (the residual's gradient is dY).
+
+    X [M, K] is the 16-bit input or its Checkpoint (only read for dW, but always needed for
+    its shape unless W is given); W [K, N] is only read for dX; Z [M, N] holds the
+    pre-activations and is needed unless activation is "none"."""
+    dt = _dtype_of(dY, "dY")
+    lddy = _matrix(dY, "dY", dY)
+    M, N = dY.shape
+    act = _activation(activation)
+    if W is not None:
+        ldw = _matrix(W, "W", dY)
+        K = W.shape[0]
+        if W.shape[1] != N:
+            raise ValueError(f"W must be [K, {N}], got {tuple(W.shape)}")
+    elif need_dX:
+        raise ValueError("dX needs W")
+    elif X is None:
+        raise ValueError("one of X and W is needed")
+    else:
+        K, ldw = (X[0] if isinstance(X, tuple) else X).shape[1], N
+    if need_dW and X is None:
+        raise ValueError("dW needs X")
+    saved = _saved(X, "X", dY, (M, K)) if need_dW else None
+    if act != LLMINT8_ACT_NONE and Z is None:
+        raise ValueError("Z is needed with an activation")
+    ldz = _matrix(Z, "Z", dY, (M, N)) if act != LLMINT8_ACT_NONE else 0
+    dX = _out(dX, "dX", dY, (M, K)) if need_dX else None
+    dW = _out(dW, "dW", dY, (K, N)) if need_dW else None
+    if need_dbias and dbias is None:
+        dbias = torch.empty((N,), dtype=torch.float32, device=dY.device)
+    if need_dbias:
+        _need_vec(dbias, "dbias", torch.float32, N)
+    else:
+        dbias = None
+    L = lib()
+    ws, nb = _workspace(workspace, L.llmint8_matmul_backward_workspace_size(M, K, N), dY.device)
+    _check(L.llmint8_matmul_backward(
+        _ptr(dY), M, N, lddy, C.byref(saved) if saved is not None else None, K, _ptr(W), ldw,
+        _ptr(Z) if ldz else None, ldz, act, dt, _ptr(dX), _ld(dX, "dX") if need_dX else 0,
+        _ptr(dW), _ld(dW, "dW") if need_dW else 0, _ptr(dbias), ws, nb, _stream(dY)))
+    return dX, dW, dbias
+
+
+def llmint8_gated_workspace_size(M: int, K: int, N: int) -> int:
+    return int(lib().llmint8_gated_workspace_size(M, K, N))
+
+
+def _gate_weights(Wg, Wu, like: torch.Tensor):
+    ldw = _matrix(Wg, "Wg", like)
+    if _matrix(Wu, "Wu", like, tuple(Wg.shape)) != ldw:
+        raise ValueError("Wg and Wu must have the same row stride")
+    return ldw
+
+
+def llmint8_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, *,
+                  activation: str = "silu", save: str = "none", H=None, workspace=None):
+    """The gated feed-forward block H = act(X Wg) * (X Wu) in one kernel: fp16 or bf16
+    X [M, K], Wg and Wu [K, N] -> H [M, N].
+
+    save "none" returns H; "full" returns (H, G, U) with the pre-activations G = X Wg and
+    U = X Wu in 16 bits, "8bit" returns them as Checkpoints."""
+    dt = _dtype_of(X, "X")
+    ldx = _matrix(X, "X", X)
+    M, K = X.shape
+    ldw = _gate_weights(Wg, Wu, X)
+    N = Wg.shape[1]
+    if Wg.shape[0] != K:
+        raise ValueError(f"Wg and Wu must be [{K}, N], got {tuple(Wg.shape)}")
+    act = _activation(activation)
+    H = _out(H, "H", X, (M, N))
+    if save not in ("none", "full", "8bit"):
+        raise ValueError("save is 'none', 'full' or '8bit'")
+    G = U = g = u = None
+    if save != "none":
+        G, U = (torch.empty((M, N), dtype=X.dtype, device=X.device) if save == "full"
+                else _new_checkpoint(M, N, X.device) for _ in range(2))
+        g, u = C.byref(_saved(G, "G", X, (M, N))), C.byref(_saved(U, "U", X, (M, N)))
+    L = lib()
+    ws, nb = _workspace(workspace, L.llmint8_gated_workspace_size(M, K, N), X.device)
+    _check(L.llmint8_gated(_ptr(X), M, K, ldx, _ptr(Wg), _ptr(Wu), ldw, N, act, dt, _ptr(H),
+                           _ld(H, "H"), g, u, ws, nb, _stream(X)))
+    return H if save == "none" else (H, G, U)
+
+
+def llmint8_gated_backward_workspace_size(M: int, K: int, N: int) -> int:
+    return int(lib().llmint8_gated_backward_workspace_size(M, K, N))
+
+
+def llmint8_gated_backward(dH: torch.Tensor, X, Wg: torch.Tensor, Wu: torch.Tensor, G, U, *,
+                           activation: str = "silu", need_dX: bool = True, need_dW: bool = True,
+                           dX=None, dWg=None, dWu=None, workspace=None):
+    """Gradients of llmint8_gated from dH [M, N]: (dX [M, K], dWg [K, N], dWu [K, N]), None
+    where not needed. X, G and U are 16-bit matrices or Checkpoints (G and U alike); X may be
+    None without need_dW."""
+    dt = _dtype_of(dH, "dH")
+    lddh = _matrix(dH, "dH", dH)
+    M, N = dH.shape
+    ldw = _gate_weights(Wg, Wu, dH)
+    K = Wg.shape[0]
+    if Wg.shape[1] != N:
+        raise ValueError(f"Wg and Wu must be [K, {N}], got {tuple(Wg.shape)}")
+    act = _activation(activation)
+    if need_dW and X is None:
+        raise ValueError("dWg and dWu need X")
+    if isinstance(G, tuple) != isinstance(U, tuple):
+        raise ValueError("G and U are both 16-bit matrices or both Checkpoints")
+    x = C.byref(_saved(X, "X", dH, (M, K))) if need_dW else None
+    g, u = _saved(G, "G", dH, (M, N)), _saved(U, "U", dH, (M, N))
+    dX = _out(dX, "dX", dH, (M, K)) if need_dX else None
+    if need_dW:
+        dWg, dWu = _out(dWg, "dWg", dH, (K, N)), _out(dWu, "dWu", dH, (K, N))
+        lddw = _ld(dWg, "dWg")
+        if _ld(dWu, "dWu") != lddw:
+            raise ValueError("dWg and dWu must have the same row stride")
+    else:
+        dWg, dWu, lddw = None, None, 0
+    L = lib()
+    ws, nb = _workspace(workspace, L.llmint8_gated_backward_workspace_size(M, K, N), dH.device)
+    _check(L.llmint8_gated_backward(
+        _ptr(dH), M, N, lddh, x, K, _ptr(Wg), _ptr(Wu), ldw, C.byref(g), C.byref(u), act, dt,
+        _ptr(dX), _ld(dX, "dX") if need_dX else 0, _ptr(dWg), _ptr(dWu), lddw, ws, nb,
+        _stream(dH)))
+    return dX, dWg, dWu

@@ -5,6 +5,7 @@ only the extern "C" entry points declared in include/llmint8.h are exported.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import hashlib
 import json
@@ -12,6 +13,7 @@ import os
 import re
 import subprocess
 import sys
+import tempfile
 import time
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -78,21 +80,35 @@ def compiler_version() -> str:
     return "; ".join(lines)
 
 
-def build(verbose: bool = False) -> str:
-    cmd = [HIPCC, *FLAGS, "-I", INCLUDE, "-I", CSRC, *sources(), "-o", LIB + ".tmp"]
+def _hipcc(args, verbose: bool) -> str:
+    """Run hipcc and return what it printed on stderr (the resource remarks)."""
     if verbose:
-        print(" ".join(cmd), flush=True)
-    proc = subprocess.run(cmd, capture_output=True, text=True)
+        print(" ".join([HIPCC, *args]), flush=True)
+    proc = subprocess.run([HIPCC, *args], capture_output=True, text=True)
     noise = ("is not a recognized feature for this target", "-Rpass-analysis=kernel-resource",
-             "remark:", "| ^", " | ")
+             "remark:", "| ^", " | ", "In file included from")
     err = "\n".join(l for l in proc.stderr.splitlines() if not any(n in l for n in noise))
     if proc.returncode != 0:
         raise RuntimeError(f"hipcc failed ({proc.returncode}):\n{err}")
     if err.strip() and verbose:
         print(err, file=sys.stderr)
+    return proc.stderr
+
+
+def build(verbose: bool = False) -> str:
+    flags = [f for f in FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = {src: os.path.join(tmp, os.path.basename(src) + ".o") for src in sources()}
+        # one hipcc per translation unit, a few at a time
+        with concurrent.futures.ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            remarks = list(pool.map(
+                lambda s: _hipcc([*flags, "-I", INCLUDE, "-I", CSRC, "-c", s, "-o", objs[s]],
+                                 verbose), objs))
+        _hipcc(["--offload-arch=gfx950", "-fPIC", "-shared", *objs.values(), "-o", LIB + ".tmp"],
+               verbose)
     os.replace(LIB + ".tmp", LIB)
     with open(RESOURCES, "w") as f:
-        json.dump(kernel_resources(proc.stderr), f, indent=1, sort_keys=True)
+        json.dump(kernel_resources("\n".join(remarks)), f, indent=1, sort_keys=True)
     record = {"source_digest": source_digest(), "library_digest": file_digest(LIB),
               "compiler": compiler_version(), "flags": FLAGS,
               "built_at": time.strftime("%Y-%m-%dT%H:%M:%SZ", time.gmtime())}

@@ -1,0 +1,88 @@
+// Internal launchers of the 16-bit feed-forward kernels: the matrix product
+// with its epilogue, the gated block, their backward passes and the 8-bit
+// activation checkpoints. Each returns hipSuccess or the error of its launch;
+// none synchronizes.
+#pragma once
+
+#include "common.hpp"
+
+namespace llmint8 {
+
+// Entries of a row that share one checkpoint scale.
+constexpr int kCkptBlock = 32;
+
+// A product of 16-bit matrices, out[i, n] = sum_k A(i, k) B(k, n), in one of
+// three operand orders (see ffn_gemm.hpp), and what happens to the sums.
+struct FfnGemm {
+  const void *a[2];   // A; the second when the reduction has two segments
+  int64_t lda;
+  const uint8_t *as;  // scales of A when it is held in 8 bits
+  int64_t ldas;
+  const void *b[2];   // B; the second for two segments, two outputs or the gated product
+  int64_t ldb;
+  int64_t M, N, K;    // rows and columns of one output, length of one segment
+  int segs;           // reduction segments (2: A0 B0 + A1 B1)
+  int outs;           // outputs side by side (2: A B0 and A B1)
+  uint16_t *y[2];
+  int64_t ldy;
+  int act;
+  const uint16_t *bias;      // [N]
+  const uint16_t *residual;  // [M x ldr]
+  int64_t ldr;
+  void *z[2];     // pre-activations out: 16 bits, or 8-bit codes where zs is set
+  int64_t ldz;
+  uint8_t *zs[2];
+  int64_t ldzs;
+  float *part;    // split reduction: partial sums [ksplit][outs or 2][M][N]
+  int ksplit;
+};
+
+// Which kernel a product takes: square tiles of `tile` rows and columns, or
+// (tile 0) the small-M kernel for at most kSkinnyMaxM rows.
+struct FfnPlan {
+  int tile;
+  int ksplit;
+};
+
+enum class FfnKind { Forward, Gated, GradX, GradW };
+
+FfnPlan ffn_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int outs);
+// bytes of the partial sums of a plan
+size_t ffn_part_bytes(const FfnPlan &p, int64_t M, int64_t N, int outs);
+
+// The plan's kernel and, for a split reduction, the pass that joins the parts.
+// dtype: 0 fp16, 1 bf16.
+hipError_t launch_ffn(FfnKind kind, int dtype, const FfnGemm &a, const FfnPlan &p, hipStream_t s);
+
+hipError_t launch_ffn_forward(int dtype, const FfnGemm &a, int tile, hipStream_t s);
+hipError_t launch_ffn_gated(int dtype, const FfnGemm &a, int tile, hipStream_t s);
+hipError_t launch_ffn_grad_x(int dtype, const FfnGemm &a, int tile, hipStream_t s);
+hipError_t launch_ffn_grad_w(int dtype, const FfnGemm &a, int tile, hipStream_t s);
+hipError_t launch_ffn_finish(int dtype, bool gated, const FfnGemm &a, hipStream_t s);
+
+// dZ = dY act'(Z) (dz null: not written; act none: dZ = dY) and the column sums
+// of dZ: dbias [N] fp32 through part, bias_rows(M, N) x N floats.
+int64_t bias_rows(int64_t M, int64_t N);
+hipError_t launch_act_grad(int dtype, int act, const uint16_t *dy, int64_t lddy, const uint16_t *z,
+                           int64_t ldz, int64_t M, int64_t N, uint16_t *dz, int64_t lddz,
+                           float *dbias, float *part, hipStream_t s);
+
+// A saved matrix: 16 bits (scales null) or 8-bit codes.
+struct Saved {
+  void *data;
+  int64_t ld;
+  uint8_t *scales;
+  int64_t lds;
+};
+
+// dG = dH U act'(G), dU = dH act(G).
+hipError_t launch_gated_grad(int dtype, int act, const uint16_t *dh, int64_t lddh, const Saved &g,
+                             const Saved &u, int64_t M, int64_t N, uint16_t *dg, uint16_t *du,
+                             int64_t ldd, hipStream_t s);
+
+hipError_t launch_ckpt_pack(int dtype, const uint16_t *x, int64_t M, int64_t K, int64_t ldx,
+                            const Saved &out, hipStream_t s);
+hipError_t launch_ckpt_unpack(int dtype, const Saved &in, int64_t M, int64_t K, uint16_t *x,
+                              int64_t ldx, hipStream_t s);
+
+}  // namespace llmint8

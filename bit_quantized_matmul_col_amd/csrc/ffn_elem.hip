@@ -1,0 +1,259 @@
+// Row-streaming kernels of the 16-bit feed-forward operators: checkpoint pack
+// and unpack, the gradient of the activation (with the bias gradient), the
+// gradient of the gate, and the pass that joins a split reduction. All are
+// bound by HBM; a thread owns 8 consecutive columns (16 bytes) of a row.
+#include "ffn_gemm.hpp"
+
+namespace llmint8 {
+
+namespace {
+
+using ffn::load_f8;
+
+constexpr int kThreads = 256;
+
+// A block covers cx chunks of 8 columns (a power of two, 8 to 256, so that the 4
+// lanes of a checkpoint block share a wave) and 256 / cx rows at a time; the
+// grid's second dimension strides over the rows.
+struct RowGrid {
+  int cx_log2;
+  dim3 grid;
+};
+
+RowGrid row_grid(int64_t M, int64_t N, int64_t max_rows) {
+  const int64_t chunks = (N + 7) / 8;
+  int lg = 3;
+  while (lg < 8 && ((int64_t)1 << lg) < chunks) ++lg;
+  const int64_t gx = (chunks + ((int64_t)1 << lg) - 1) >> lg, ry = kThreads >> lg;
+  int64_t gy = (M + ry - 1) / ry;
+  if (gy > max_rows) gy = max_rows;
+  return RowGrid{lg, dim3((unsigned)gx, (unsigned)gy)};
+}
+
+constexpr int64_t kMaxGridY = 65535;
+
+// Calls f(i, n, in) for the rows i and the first column n of this thread's
+// chunks; in is false for a chunk past N (its lanes still take part in shuffles).
+template <class F>
+__device__ inline void for_rows(int cx_log2, int64_t M, int64_t N, F f) {
+  const int t = threadIdx.x;
+  const int64_t n = (((int64_t)blockIdx.x << cx_log2) + (t & ((1 << cx_log2) - 1))) * 8;
+  const int64_t ry = kThreads >> cx_log2;
+  for (int64_t i = blockIdx.y * ry + (t >> cx_log2); i < M; i += gridDim.y * ry) f(i, n, n < N);
+}
+
+// 8 entries of a saved matrix. The scale byte is shared by 4 lanes.
+template <class T, bool Q8>
+__device__ inline void load_saved(const Saved &s, int64_t i, int64_t n, float *v) {
+  if constexpr (Q8) {
+    const u32x2 w = *(const u32x2 *)((const uint8_t *)s.data + i * s.ld + n);
+    const float scale = ckpt_scale(s.scales[i * s.lds + n / kCkptBlock]);
+    ckpt_value4(w[0], scale, v);
+    ckpt_value4(w[1], scale, v + 4);
+  } else {
+    load8<T>((const uint16_t *)s.data + i * s.ld + n, v);
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void k_ckpt_pack(const uint16_t *x, int64_t M, int64_t K,
+                                                        int64_t ldx, Saved out, int cx_log2) {
+  for_rows(cx_log2, M, K, [&](int64_t i, int64_t n, bool in) {
+    float v[8] = {0.f};
+    if (in) load8<T>(x + i * ldx + n, v);
+    ffn::save8<T>(out.data, out.ld, out.scales, out.lds, i, n, in, v);
+  });
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void k_ckpt_unpack(Saved in8, int64_t M, int64_t K,
+                                                          uint16_t *x, int64_t ldx, int cx_log2) {
+  for_rows(cx_log2, M, K, [&](int64_t i, int64_t n, bool in) {
+    if (!in) return;
+    float v[8];
+    load_saved<T, true>(in8, i, n, v);
+    store8<T>(x + i * ldx + n, v);
+  });
+}
+
+template <class T, bool Q8>
+__global__ __launch_bounds__(kThreads) void k_gated_grad(int act, const uint16_t *dh, int64_t lddh,
+                                                         Saved g, Saved u, int64_t M, int64_t N,
+                                                         uint16_t *dg, uint16_t *du, int64_t ldd,
+                                                         int cx_log2) {
+  for_rows(cx_log2, M, N, [&](int64_t i, int64_t n, bool in) {
+    if (!in) return;
+    float h[8], gv[8], uv[8];
+    load8<T>(dh + i * lddh + n, h);
+    load_saved<T, Q8>(g, i, n, gv);
+    load_saved<T, Q8>(u, i, n, uv);
+    with_act(act, [&](auto tag) {
+      constexpr int A = decltype(tag)::value;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float z = gv[e];
+        gv[e] = h[e] * uv[e] * act_grad<A>(z);
+        uv[e] = h[e] * act_of<A>(z);
+      }
+    });
+    store8<T>(dg + i * ldd + n, gv);
+    store8<T>(du + i * ldd + n, uv);
+  });
+}
+
+// dz = dy act'(z) and, with part, the column sums of dz over this block's rows:
+// each thread sums its own rows, LDS joins the block's, k_bias_join the blocks'.
+// Always in the same order, so the result does not vary.
+template <class T>
+__global__ __launch_bounds__(kThreads) void k_act_grad(int act, const uint16_t *dy, int64_t lddy,
+                                                       const uint16_t *z, int64_t ldz, int64_t M,
+                                                       int64_t N, uint16_t *dz, int64_t lddz,
+                                                       float *part, int cx_log2) {
+  float sum[8] = {0.f};
+  for_rows(cx_log2, M, N, [&](int64_t i, int64_t n, bool in) {
+    if (!in) return;
+    float d[8];
+    load8<T>(dy + i * lddy + n, d);
+    if (act != LLMINT8_ACT_NONE) {
+      float zv[8];
+      load8<T>(z + i * ldz + n, zv);
+      with_act(act, [&](auto tag) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] *= act_grad<decltype(tag)::value>(zv[e]);
+      });
+    }
+    if (dz) store8<T>(dz + i * lddz + n, d);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += d[e];
+  });
+  if (!part) return;
+  __shared__ float s[kThreads][8];
+  const int t = threadIdx.x, cx = 1 << cx_log2;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[t][e] = sum[e];
+  __syncthreads();
+  if (t < cx) {
+    const int64_t n = (((int64_t)blockIdx.x << cx_log2) + t) * 8;
+    if (n < N) {
+      for (int r = t + cx; r < kThreads; r += cx)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += s[r][e];
+      ffn::store_f8(part + (int64_t)blockIdx.y * N + n, sum);
+    }
+  }
+}
+
+// dbias[n] = sum of the row blocks' partial sums; a block takes 64 columns, its
+// 4 waves a quarter of the row blocks each.
+__global__ __launch_bounds__(kThreads) void k_bias_join(const float *part, int64_t rows, int64_t N,
+                                                        float *dbias) {
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int64_t n = (int64_t)blockIdx.x * 64 + lane;
+  float sum = 0.f;
+  if (n < N)
+    for (int64_t r = wv; r < rows; r += 4) sum += part[r * N + n];
+  __shared__ float s[4][64];
+  s[wv][lane] = sum;
+  __syncthreads();
+  if (wv == 0 && n < N) dbias[n] = (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]);
+}
+
+// Joins the partial sums of a split reduction (in the order of the parts) and
+// runs the epilogue.
+template <class T, bool GATED>
+__global__ __launch_bounds__(kThreads) void k_ffn_finish(FfnGemm a, int cx_log2) {
+  const int64_t plane = a.M * a.N;
+  const int out = blockIdx.z;
+  for_rows(cx_log2, a.M, a.N, [&](int64_t i, int64_t n, bool in) {
+    float v[8] = {0.f}, u[8] = {0.f};
+    if (in) {
+      const int per = GATED ? 2 : a.outs;
+      const float *p = a.part + (GATED ? 0 : out) * plane + i * a.N + n;
+      for (int s = 0; s < a.ksplit; ++s, p += per * plane) {
+        float x[8];
+        load_f8(p, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += x[e];
+        if constexpr (GATED) {
+          load_f8(p + plane, x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] += x[e];
+        }
+      }
+    }
+    if constexpr (GATED)
+      ffn::finish_gated<T>(a, i, n, in, v, u);
+    else if (in)
+      ffn::finish_forward<T>(a, out, i, n, v);
+  });
+}
+
+}  // namespace
+
+hipError_t launch_ckpt_pack(int dtype, const uint16_t *x, int64_t M, int64_t K, int64_t ldx,
+                            const Saved &out, hipStream_t s) {
+  const RowGrid g = row_grid(M, K, kMaxGridY);
+  auto *kern = dtype == LLMINT8_FP16 ? k_ckpt_pack<Half> : k_ckpt_pack<Bfloat>;
+  hipLaunchKernelGGL(kern, g.grid, dim3(kThreads), 0, s, x, M, K, ldx, out, g.cx_log2);
+  return hipGetLastError();
+}
+
+hipError_t launch_ckpt_unpack(int dtype, const Saved &in, int64_t M, int64_t K, uint16_t *x,
+                              int64_t ldx, hipStream_t s) {
+  const RowGrid g = row_grid(M, K, kMaxGridY);
+  auto *kern = dtype == LLMINT8_FP16 ? k_ckpt_unpack<Half> : k_ckpt_unpack<Bfloat>;
+  hipLaunchKernelGGL(kern, g.grid, dim3(kThreads), 0, s, in, M, K, x, ldx, g.cx_log2);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_grad(int dtype, int act, const uint16_t *dh, int64_t lddh, const Saved &g,
+                             const Saved &u, int64_t M, int64_t N, uint16_t *dg, uint16_t *du,
+                             int64_t ldd, hipStream_t s) {
+  const RowGrid r = row_grid(M, N, kMaxGridY);
+  auto *kern = dtype == LLMINT8_FP16
+                   ? (g.scales ? k_gated_grad<Half, true> : k_gated_grad<Half, false>)
+                   : (g.scales ? k_gated_grad<Bfloat, true> : k_gated_grad<Bfloat, false>);
+  hipLaunchKernelGGL(kern, r.grid, dim3(kThreads), 0, s, act, dh, lddh, g, u, M, N, dg, du, ldd,
+                     r.cx_log2);
+  return hipGetLastError();
+}
+
+// Row blocks of the bias gradient: enough blocks for the chip (1024 in all), at
+// least 16 rows a thread where there are as many.
+int64_t bias_rows(int64_t M, int64_t N) {
+  const RowGrid g = row_grid(M, N, kMaxGridY);
+  const int64_t ry = kThreads >> g.cx_log2;
+  int64_t rows = (M + 16 * ry - 1) / (16 * ry);
+  const int64_t want = (1024 + g.grid.x - 1) / g.grid.x;
+  if (rows > want) rows = want;
+  return rows;
+}
+
+hipError_t launch_act_grad(int dtype, int act, const uint16_t *dy, int64_t lddy, const uint16_t *z,
+                           int64_t ldz, int64_t M, int64_t N, uint16_t *dz, int64_t lddz,
+                           float *dbias, float *part, hipStream_t s) {
+  const int64_t rows = dbias ? bias_rows(M, N) : kMaxGridY;
+  const RowGrid g = row_grid(M, N, rows);
+  auto *kern = dtype == LLMINT8_FP16 ? k_act_grad<Half> : k_act_grad<Bfloat>;
+  hipLaunchKernelGGL(kern, g.grid, dim3(kThreads), 0, s, act, dy, lddy, z, ldz, M, N, dz, lddz,
+                     dbias ? part : nullptr, g.cx_log2);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && dbias) {
+    hipLaunchKernelGGL(k_bias_join, dim3((unsigned)((N + 63) / 64)), dim3(kThreads), 0, s, part,
+                       (int64_t)g.grid.y, N, dbias);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+hipError_t launch_ffn_finish(int dtype, bool gated, const FfnGemm &a, hipStream_t s) {
+  RowGrid g = row_grid(a.M, a.N, kMaxGridY);
+  if (!gated) g.grid.z = a.outs;
+  auto *kern = dtype == LLMINT8_FP16
+                   ? (gated ? k_ffn_finish<Half, true> : k_ffn_finish<Half, false>)
+                   : (gated ? k_ffn_finish<Bfloat, true> : k_ffn_finish<Bfloat, false>);
+  hipLaunchKernelGGL(kern, g.grid, dim3(kThreads), 0, s, a, g.cx_log2);
+  return hipGetLastError();
+}
+
+}  // namespace llmint8

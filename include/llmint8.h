@@ -286,6 +286,126 @@ int llmint8_linear_fp8(const uint16_t *X, int64_t M, int64_t K, int64_t ldx,
                        void *workspace, size_t workspace_bytes, void *stream,
                        const llmint8_linear_opts *opts);
 
+/*
+ * 16-bit feed-forward operators: the layers of the same block that stay in 16
+ * bits, and its training step. fp16 or bf16 (`dtype`), weights [K x N] as
+ * above, so that a trained W goes to llmint8_quantize_colwise unchanged. Sums
+ * are fp32; every result is rounded once, where it is stored.
+ * Shape rules of this section: K and N are multiples of 8 (M is any), leading
+ * dimensions of 16-bit matrices are multiples of 8 and below 2^21, those of
+ * 8-bit codes multiples of 16; pointers 16-byte aligned (scales: any). Sizes
+ * below 1 are LLMINT8_ERR_INVALID_ARG. Unlike in the int8 calls, infinities and
+ * NaNs go through as the formulas have them and stay in the rows (and, for a
+ * weight gradient, the columns) that they enter.
+ */
+#define LLMINT8_FP16 0
+#define LLMINT8_BF16 1
+
+/* Activations: z; max(z, 0); z (1 + erf(z / sqrt 2)) / 2;
+ * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2; z / (1 + e^-z). */
+#define LLMINT8_ACT_NONE 0
+#define LLMINT8_ACT_RELU 1
+#define LLMINT8_ACT_GELU 2
+#define LLMINT8_ACT_GELU_TANH 3
+#define LLMINT8_ACT_SILU 4
+
+/*
+ * A matrix kept from the forward for the backward pass: in 16 bits (scales
+ * NULL, ld in elements) or as an 8-bit checkpoint (data: int8 codes).
+ * Checkpoint format: 32 consecutive entries of a row (the last block of a row
+ * may be shorter) share the scale 2^e, e = max(floor(log2 max|x|) - 6, -127),
+ * held as the byte e + 127; code = clamp(rint(x 2^-e), -127, 127), ties to
+ * even, and the entry stands for code 2^e. That value is exact in fp16 and bf16.
+ * A block that holds an infinity or a NaN takes the byte 255 and stands for NaN.
+ *   data     codes [M x ld], ld a multiple of 16; calls read rows up to the
+ *            next multiple of 16 entries.
+ *   scales   [M x ld_scales] bytes, ld_scales >= ceil(columns / 32).
+ */
+typedef struct llmint8_saved {
+  void *data;
+  int64_t ld;
+  uint8_t *scales;
+  int64_t ld_scales;
+} llmint8_saved;
+
+/* 16-bit X [M x K] to an 8-bit checkpoint, and what the checkpoint stands for
+ * back to 16 bits. `out` and `in` must have scales. */
+int llmint8_checkpoint_pack(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, int dtype,
+                            const llmint8_saved *out, void *stream);
+int llmint8_checkpoint_unpack(const llmint8_saved *in, int64_t M, int64_t K, int dtype,
+                              uint16_t *X, int64_t ldx, void *stream);
+
+/*
+ * Y = act(Z) + R with Z = X . W + bias, one product with the rest in its epilogue.
+ *   opts  may be NULL (Y = X . W). Zero-initialize, set struct_size, fill in:
+ *     activation  LLMINT8_ACT_*.
+ *     bias        optional [N].
+ *     residual    optional R [M x N], leading dimension ldr.
+ *     Z           optional output [M x N], leading dimension ldz: the
+ *                 pre-activations, for the backward pass.
+ *   workspace  llmint8_matmul_workspace_size(M, K, N) bytes (may be 0: NULL then).
+ */
+typedef struct llmint8_matmul_opts {
+  size_t struct_size;
+  int activation;
+  const uint16_t *bias;
+  const uint16_t *residual;
+  int64_t ldr;
+  uint16_t *Z;
+  int64_t ldz;
+} llmint8_matmul_opts;
+size_t llmint8_matmul_workspace_size(int64_t M, int64_t K, int64_t N);
+int llmint8_matmul(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, const uint16_t *W,
+                   int64_t ldw, int64_t N, int dtype, uint16_t *Y, int64_t ldy,
+                   const llmint8_matmul_opts *opts, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
+/*
+ * Gradients of llmint8_matmul: with dZ = dY * act'(Z) (rounded to 16 bits, the
+ * products' operand),
+ *   dX = dZ . W^T [M x K],  dW = X^T . dZ [K x N],  dbias = column sums of dZ
+ * (dbias fp32, from the unrounded dZ). The residual's gradient is dY itself.
+ * Each output may be NULL: not computed. X may be NULL without dW, W without dX,
+ * Z when activation is LLMINT8_ACT_NONE (it is not read then).
+ *   X  16 bits or an 8-bit checkpoint.
+ *   workspace  llmint8_matmul_backward_workspace_size(M, K, N) bytes.
+ */
+size_t llmint8_matmul_backward_workspace_size(int64_t M, int64_t K, int64_t N);
+int llmint8_matmul_backward(const uint16_t *dY, int64_t M, int64_t N, int64_t lddy,
+                            const llmint8_saved *X, int64_t K, const uint16_t *W, int64_t ldw,
+                            const uint16_t *Z, int64_t ldz, int activation, int dtype,
+                            uint16_t *dX, int64_t lddx, uint16_t *dW, int64_t lddw, float *dbias,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gated feed-forward block: H = act(G) * U with G = X . Wg and U = X . Wu,
+ * both products in one kernel. Wg and Wu share the leading dimension ldw.
+ *   G, U  both NULL, or both given: the pre-activations out, both in 16 bits or
+ *         both as 8-bit checkpoints (taken from the fp32 sums).
+ *   workspace  llmint8_gated_workspace_size(M, K, N) bytes.
+ */
+size_t llmint8_gated_workspace_size(int64_t M, int64_t K, int64_t N);
+int llmint8_gated(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, const uint16_t *Wg,
+                  const uint16_t *Wu, int64_t ldw, int64_t N, int activation, int dtype,
+                  uint16_t *H, int64_t ldh, const llmint8_saved *G, const llmint8_saved *U,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of llmint8_gated: dG = dH * U * act'(G) and dU = dH * act(G)
+ * (rounded to 16 bits, the products' operands),
+ *   dX = dG . Wg^T + dU . Wu^T,  dWg = X^T . dG,  dWu = X^T . dU.
+ * dX may be NULL (Wg and Wu are not read then); dWg and dWu both or neither
+ * (X is not read then). G and U as the forward pass saved them, X likewise.
+ *   workspace  llmint8_gated_backward_workspace_size(M, K, N) bytes.
+ */
+size_t llmint8_gated_backward_workspace_size(int64_t M, int64_t K, int64_t N);
+int llmint8_gated_backward(const uint16_t *dH, int64_t M, int64_t N, int64_t lddh,
+                           const llmint8_saved *X, int64_t K, const uint16_t *Wg,
+                           const uint16_t *Wu, int64_t ldw, const llmint8_saved *G,
+                           const llmint8_saved *U, int activation, int dtype, uint16_t *dX,
+                           int64_t lddx, uint16_t *dWg, uint16_t *dWu, int64_t lddw,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *llmint8_status_string(int status);
 
