@@ -16,8 +16,6 @@ constexpr int kCkptBlock = 32;
 struct FfnGemm {
   const void *a[2];   // A; the second when the reduction has two segments
   int64_t lda;
-  const uint8_t *as;  // scales of A when it is held in 8 bits
-  int64_t ldas;
   const void *b[2];   // B; the second for two segments, two outputs or the gated product
   int64_t ldb;
   int64_t M, N, K;    // rows and columns of one output, length of one segment
@@ -38,7 +36,7 @@ struct FfnGemm {
 };
 
 // Which kernel a product takes: square tiles of `tile` rows and columns, or
-// (tile 0) the small-M kernel for at most kSkinnyMaxM rows.
+// (tile 0) the kernel for few rows.
 struct FfnPlan {
   int tile;
   int ksplit;
@@ -58,6 +56,7 @@ hipError_t launch_ffn_forward(int dtype, const FfnGemm &a, int tile, hipStream_t
 hipError_t launch_ffn_gated(int dtype, const FfnGemm &a, int tile, hipStream_t s);
 hipError_t launch_ffn_grad_x(int dtype, const FfnGemm &a, int tile, hipStream_t s);
 hipError_t launch_ffn_grad_w(int dtype, const FfnGemm &a, int tile, hipStream_t s);
+hipError_t launch_ffn_skinny(int dtype, bool gated, const FfnGemm &a, hipStream_t s);
 hipError_t launch_ffn_finish(int dtype, bool gated, const FfnGemm &a, hipStream_t s);
 
 // dZ = dY act'(Z) (dz null: not written; act none: dZ = dY) and the column sums

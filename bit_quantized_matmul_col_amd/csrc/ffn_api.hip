@@ -11,7 +11,7 @@ using namespace llmint8;
 
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t)1 << 31;
+constexpr int64_t kMaxDim = (int64_t)1 << 30;  // stage offsets are 32-bit
 constexpr int64_t kMaxLd = (int64_t)1 << 21;  // 256 rows x 2 bytes x 2^21 = 2^30
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -66,10 +66,11 @@ int check_workspace(const void *ws, size_t bytes, size_t need) {
 Saved saved_of(const llmint8_saved *s) { return Saved{s->data, s->ld, s->scales, s->ld_scales}; }
 
 // Workspace of a backward pass: the 16-bit operands of its products (`grads` of
-// them), the bias gradient's partial sums, and the partial sums of the split
-// products (one region, the products run one after the other).
+// them), a checkpointed X expanded to 16 bits, the bias gradient's partial sums,
+// and the partial sums of the split products (one region, the products run one
+// after the other).
 struct BackLayout {
-  size_t dz, bias, part, total;
+  size_t dz, x, bias, part, total;
   FfnPlan px, pw;
 };
 
@@ -80,6 +81,8 @@ BackLayout back_layout(int64_t M, int64_t K, int64_t N, int grads) {
   size_t o = 0;
   L.dz = o;
   o += up((size_t)grads * M * pitch8(N) * 2);
+  L.x = o;
+  o += up((size_t)M * K * 2);
   L.bias = o;
   if (grads == 1) o += up((size_t)bias_rows(M, N) * N * 4);
   L.part = o;
@@ -103,12 +106,21 @@ hipError_t grad_x(int dtype, const uint16_t *const *dz, int64_t lddz, const uint
   return launch_ffn(FfnKind::GradX, dtype, a, p, s);
 }
 
-// dW_i = X^T dZ_i for the outputs side by side.
-hipError_t grad_w(int dtype, const llmint8_saved &X, const uint16_t *const *dz, int64_t lddz,
-                  int outs, int64_t M, int64_t K, int64_t N, uint16_t *const *dW, int64_t lddw,
-                  const FfnPlan &p, float *part, hipStream_t s) {
+// dW_i = X^T dZ_i for the outputs side by side. A checkpointed X is expanded into
+// `room` first, exactly: a pass of 3 bytes an entry against a product of 2 N or
+// 4 N operations an entry. Expanding the codes inside the product's tiles instead
+// (8-bit loads to registers, 16-bit stores to LDS) cost more than the pass at
+// 2048 x 4096 x 11008: 438 against 412 + 6 us.
+hipError_t grad_w(int dtype, const llmint8_saved &X, uint16_t *room, const uint16_t *const *dz,
+                  int64_t lddz, int outs, int64_t M, int64_t K, int64_t N, uint16_t *const *dW,
+                  int64_t lddw, const FfnPlan &p, float *part, hipStream_t s) {
   FfnGemm a{};
-  a.a[0] = X.data, a.lda = X.ld, a.as = X.scales, a.ldas = X.ld_scales;
+  a.a[0] = X.data, a.lda = X.ld;
+  if (X.scales) {
+    const hipError_t e = launch_ckpt_unpack(dtype, saved_of(&X), M, K, room, K, s);
+    if (e != hipSuccess) return e;
+    a.a[0] = room, a.lda = K;
+  }
   for (int i = 0; i < outs; ++i) a.b[i] = dz[i], a.y[i] = dW[i];
   a.ldb = lddz;
   a.M = K, a.N = N, a.K = M;
@@ -219,7 +231,7 @@ LLMINT8_EXPORT int llmint8_matmul_backward(const uint16_t *dY, int64_t M, int64_
                         lddz, dbias, (float *)(ws + L.bias), s);
   if (e == hipSuccess && dX)
     e = grad_x(dtype, &dz, lddz, &W, ldw, 1, M, K, N, dX, lddx, L.px, part, s);
-  if (e == hipSuccess && dW) e = grad_w(dtype, *X, &dz, lddz, 1, M, K, N, &dW, lddw, L.pw, part, s);
+  if (e == hipSuccess && dW) e = grad_w(dtype, *X, (uint16_t *)(ws + L.x), &dz, lddz, 1, M, K, N, &dW, lddw, L.pw, part, s);
   return hip_status(e);
 }
 
@@ -301,6 +313,6 @@ LLMINT8_EXPORT int llmint8_gated_backward(const uint16_t *dH, int64_t M, int64_t
                                    du, lddz, s);
   if (e == hipSuccess && dX)
     e = grad_x(dtype, dz, lddz, w, ldw, 2, M, K, N, dX, lddx, L.px, part, s);
-  if (e == hipSuccess && dWg) e = grad_w(dtype, *X, dz, lddz, 2, M, K, N, dw, lddw, L.pw, part, s);
+  if (e == hipSuccess && dWg) e = grad_w(dtype, *X, (uint16_t *)(ws + L.x), dz, lddz, 2, M, K, N, dw, lddw, L.pw, part, s);
   return hip_status(e);
 }

@@ -47,61 +47,89 @@ namespace ffn {
 using gemm_detail::lptr_t;
 using gemm_detail::make_rsrc;
 using gemm_detail::rsrc_t;
-using gemm_detail::tile_of_block;
 using gemm_detail::wait_vm;
 
 constexpr int kStep = 64;  // reduction steps per stage
+constexpr int kStages = 2;  // LDS ring
 constexpr int kOob = (int)0x80000000;  // an offset past the end of every resource
 
-enum class Lay { RowK, ColK, ColK8 };
+// The wave's number in its block, known to be the same for all its lanes.
+__device__ inline int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// First of n stages that part `split` of `parts` takes.
+__device__ inline int part_begin(int n, int split, int parts) {
+  return (int)((uint64_t)n * split / (uint32_t)parts);
+}
+
+// Tile of block v: the blocks of one XCD (they are dealt out round robin) take
+// consecutive tiles, in groups of up to 8 tile rows, so that its L2 serves the
+// operand tiles that they share.
+__device__ inline void tile_at(uint32_t bid, uint32_t tiles_m, uint32_t tiles_n, int &tm, int &tn) {
+  constexpr uint32_t X = gemm_detail::kXcds, GM = gemm_detail::kGroupM;
+  const uint32_t nb = tiles_m * tiles_n, x = bid % X, rem = nb % X;
+  const uint32_t v = x * (nb / X) + (x < rem ? x : rem) + bid / X;
+  const uint32_t first = v / (GM * tiles_n) * GM, in = v % (GM * tiles_n);
+  const uint32_t gm = tiles_m - first < GM ? tiles_m - first : GM;
+  tm = (int)(first + in % gm);
+  tn = (int)(in / gm);
+}
+
+enum class Lay { RowK, ColK };
 
 __device__ inline int clip31(int64_t bytes) {
   return (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff);
 }
 
-// ROWS output rows (or columns) x 64 reduction steps, reduction contiguous.
+// ROWS output rows (or columns) x kStep reduction steps, reduction contiguous.
 template <int ROWS, int NW>
 struct RowKTile {
-  static constexpr int BYTES = ROWS * 128;
-  static constexpr int G = ROWS / (8 * NW);  // 1 KB loads per wave per stage
-  static constexpr int REGS = 1;             // LDS address registers per fragment row block
-  int64_t bytes;  // of the tile's rows, from the first element to the last
+  static constexpr int PITCH = kStep * 2;    // bytes of a stored row
+  static constexpr int BYTES = ROWS * PITCH;
+  static constexpr int CH = PITCH / 16;      // chunks per stored row
+  static constexpr int RPI = 64 / CH;        // rows per 1 KB load
+  static constexpr int G = ROWS / (RPI * NW);  // loads per wave per stage
+  int bytes;  // of the tile's rows, from the first element to the last
   int voff[G];
   int chunk;      // first reduction step of this lane's chunk within a stage
 
-  // mat: the first row of the tile; rows: rows of the matrix from there on.
+  __device__ static int key(int r) { return CH == 8 ? (r >> 1) & 7 : (r >> 2) & 3; }
+
+  // rows: rows of the matrix from the tile's first on; len: the reduction length.
   __device__ void init(int64_t ld, int64_t rows, int64_t len) {
     rows = rows < ROWS ? rows : ROWS;
-    bytes = ((rows - 1) * ld + len) * 2;
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    chunk = 0;
+    bytes = (int)((rows - 1) * ld + len) * 2;
+    const int lane = threadIdx.x & 63, wv = wave_id();
 #pragma unroll
     for (int j = 0; j < G; ++j) {
-      const int r = (wv + NW * j) * 8 + lane / 8;
-      const int c = (lane % 8) ^ ((r >> 1) & 7);
+      const int r = (wv + NW * j) * RPI + lane / CH;
+      const int c = (lane % CH) ^ key(r);
       voff[j] = r * (int)ld * 2 + 16 * c;
       chunk = 8 * c;  // the same for every j: the key repeats every 16 rows
     }
   }
-  static_assert(NW % 2 == 0, "the chunk key must not depend on j");
+  static_assert((RPI * NW) % 16 == 0, "the chunk key must not depend on j");
 
-  // Groups j0 .. j1 - 1 of the stage starting at reduction step k.
-  __device__ void load(const void *mat, int64_t len, int64_t, uint8_t *stage, int64_t k, int j0,
-                       int j1) const {
-    const int wv = threadIdx.x >> 6;
-    const rsrc_t rs = make_rsrc((const uint8_t *)mat + 2 * k, clip31(bytes - 2 * k));
-    const bool in = k + chunk < len;
-#pragma unroll
-    for (int j = 0; j < G; ++j)
-      if (j >= j0 && j < j1)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lptr_t)(stage + (wv + NW * j) * 1024), 16,
-                                                 in ? voff[j] : kOob, 0, 0, 0);
+  // What the loads of one stage share: the resource from reduction step k on
+  // (mat: the tile's first row), and whether this lane's chunk is within the
+  // reduction length.
+  struct Stage {
+    rsrc_t rs;
+    bool in;
+  };
+  __device__ Stage stage(const uint8_t *mat, int64_t, int k, int len) const {
+    const int left = bytes - 2 * k;  // empty past the end
+    return Stage{make_rsrc(mat + 2 * (int64_t)k, left > 0 ? left : 0), k + chunk < len};
+  }
+  // the j-th load of the stage, to LDS at `to`
+  __device__ void load(const Stage &st, uint8_t *to, int j) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rs, (lptr_t)(to + (wave_id() + NW * j) * 1024), 16,
+                                             st.in ? voff[j] : kOob, 0, 0, 0);
   }
 
   // Fragment of 32 rows from row0 for reduction steps 16 ks .. 16 ks + 15.
   __device__ static s16x8 frag(const uint8_t *tile, int row0, int ks, int lane) {
     const int r = row0 + (lane & 31);
-    return *(const s16x8 *)(tile + r * 128 + 16 * ((2 * ks + (lane >> 5)) ^ ((r >> 1) & 7)));
+    return *(const s16x8 *)(tile + r * PITCH + 16 * ((2 * ks + (lane >> 5)) ^ key(r)));
   }
 };
 
@@ -116,22 +144,22 @@ __device__ inline s16x4 read_tr16(tr_ptr_t __restrict p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
 }
 
-// 64 reduction steps x COLS output rows (or columns), reduction strided.
+// kStep reduction steps x COLS output rows (or columns), reduction strided.
 template <int COLS, int NW>
 struct ColKTile {
-  static constexpr int BYTES = COLS * 128;
-  static constexpr int PITCH = COLS * 2;
+  static constexpr int PITCH = COLS * 2;     // bytes of a stored row
+  static constexpr int BYTES = kStep * PITCH;
   static constexpr int CH = COLS / 8;      // chunks per stored row
   static constexpr int RPI = 64 / CH;      // stored rows per 1 KB load
   static constexpr int G = kStep / (RPI * NW);
   int voff[G];
-  int64_t cols;  // columns of the matrix from the tile's first on
+  int cols;  // columns of the matrix from the tile's first on
 
   // Rows of 8 chunks: rows r and r + 1 lie in opposite halves of the banks already.
   __device__ static int key(int r) { return CH >= 16 ? 4 * (r & 3) : 4 * ((r >> 1) & 1); }
 
   __device__ void init(int64_t ld, int64_t ncols, int64_t) {
-    cols = ncols;
+    cols = (int)ncols;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
 #pragma unroll
     for (int j = 0; j < G; ++j) {
@@ -141,18 +169,18 @@ struct ColKTile {
   }
 
   // mat: element (0, first column of the tile). The resource ends with the last
-  // column of the stage's last row of the matrix.
-  __device__ void load(const void *mat, int64_t len, int64_t ld, uint8_t *stage, int64_t k, int j0,
-                       int j1) const {
-    const int wv = threadIdx.x >> 6;
-    const int64_t rows = len - k < kStep ? len - k : kStep;
-    const rsrc_t rs = make_rsrc((const uint8_t *)mat + 2 * k * ld,
-                                clip31(((rows - 1) * ld + cols) * 2));
-#pragma unroll
-    for (int j = 0; j < G; ++j)
-      if (j >= j0 && j < j1)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lptr_t)(stage + (wv + NW * j) * 1024), 16,
-                                                 voff[j], 0, 0, 0);
+  // column of the stage's last row of the matrix (it is empty past the length).
+  struct Stage {
+    rsrc_t rs;
+  };
+  __device__ Stage stage(const uint8_t *mat, int64_t ld, int k, int len) const {
+    const int left = len - k, rows = left < kStep ? left : kStep;
+    const int n = ((rows - 1) * (int)ld + cols) * 2;
+    return Stage{make_rsrc(mat + 2 * (int64_t)k * ld, n > 0 ? n : 0)};
+  }
+  __device__ void load(const Stage &st, uint8_t *to, int j) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rs, (lptr_t)(to + (wave_id() + NW * j) * 1024), 16,
+                                             voff[j], 0, 0, 0);
   }
 
   __device__ static s16x8 frag(const uint8_t *tile, int col0, int ks, int lane) {
@@ -162,53 +190,6 @@ struct ColKTile {
                        16 * (c ^ key(i >> 2)) + 8 * (i & 1);
     const s16x4 lo = read_tr16((tr_ptr_t)p), hi = read_tr16((tr_ptr_t)(p + 4 * PITCH));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-  }
-};
-
-// ColKTile filled from 8-bit codes through registers: fetch() starts the loads
-// of a stage, commit() expands them into LDS. Rows of codes are read to the next
-// multiple of 16 entries (their pitch is one); what lies there past the last
-// column only reaches outputs that are not stored.
-template <class T, int COLS, int NW>
-struct ColK8Tile : ColKTile<COLS, NW> {
-  using Base = ColKTile<COLS, NW>;
-  static constexpr int CPR = COLS / 16;               // 16-code chunks per row
-  static constexpr int J = kStep * CPR / (64 * NW);   // chunks per thread
-  static constexpr int RPJ = 64 * NW / CPR;           // rows between a thread's chunks
-  u32x4 q[J];
-  uint32_t sc[J];
-
-  __device__ void fetch(const void *mat, int64_t ld, const uint8_t *scales, int64_t lds,
-                        int64_t len, int64_t k) {
-    const int t = threadIdx.x, r0 = t / CPR, c = t % CPR;
-    const int64_t rows = len - k < kStep ? len - k : kStep;
-    const rsrc_t rs = make_rsrc((const uint8_t *)mat + k * ld,
-                                clip31((rows - 1) * ld + (Base::cols + 15) / 16 * 16));
-    const rsrc_t rc = make_rsrc(scales + k * lds,
-                                clip31((rows - 1) * lds + (Base::cols + kCkptBlock - 1) / kCkptBlock));
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int r = r0 + RPJ * j;
-      q[j] = __builtin_bit_cast(
-          u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, r * (int)ld + 16 * c, 0, 0));
-      sc[j] = __builtin_amdgcn_raw_buffer_load_b8(rc, r * (int)lds + c / 2, 0, 0);
-    }
-  }
-
-  __device__ void commit(uint8_t *stage) const {
-    const int t = threadIdx.x, r0 = t / CPR, c = t % CPR;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int r = r0 + RPJ * j;
-      const float scale = ckpt_scale(sc[j] & 0xffu);
-      float v[16];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ckpt_value4(q[j][e], scale, v + 4 * e);
-      uint8_t *row = stage + r * Base::PITCH;
-      const int key = Base::key(r);
-      store8<T>((uint16_t *)(row + 16 * ((2 * c) ^ key)), v);
-      store8<T>((uint16_t *)(row + 16 * ((2 * c + 1) ^ key)), v + 8);
-    }
   }
 };
 
@@ -282,17 +263,13 @@ __device__ inline void load_f8(const float *p, float *v) {
 
 // ---- kernel ---------------------------------------------------------------------------
 
-template <class T, Lay L, int N, int NW>
+template <Lay L, int N, int NW>
 struct TileOf {
   using type = RowKTile<N, NW>;
 };
-template <class T, int N, int NW>
-struct TileOf<T, Lay::ColK, N, NW> {
+template <int N, int NW>
+struct TileOf<Lay::ColK, N, NW> {
   using type = ColKTile<N, NW>;
-};
-template <class T, int N, int NW>
-struct TileOf<T, Lay::ColK8, N, NW> {
-  using type = ColK8Tile<T, N, NW>;
 };
 
 // One launch shape: operand orders, block tile, waves.
@@ -306,45 +283,47 @@ struct Cfg {
   static constexpr int WM = BM / NWM, WN = BN / NWN, MI = WM / 32, NI = WN / 32;
   // columns of one output that a block covers, and of its B tile
   static constexpr int OUTN = GATED ? BN / 2 : BN, BCOLS = OUTN;
-  static constexpr int STAGE = (BM + BN) * 128;
+  static constexpr int STAGE = (BM + BN) * kStep * 2;
   static constexpr int SLABP = WN + 4;  // fp32 pitch of the epilogue's rows
   static constexpr int SLABS = NW * 32 * SLABP * 4;
-  static constexpr int LDS = 2 * STAGE > SLABS ? 2 * STAGE : SLABS;
+  static constexpr int LDS = kStages * STAGE > SLABS ? kStages * STAGE : SLABS;
   static_assert(!GATED || NI == 2, "a gated wave holds 32 columns of each product");
 };
 
 template <class C>
-__device__ __forceinline__ void ffn_tile(const FfnGemm &a, int64_t bid, uint8_t *smem) {
+__device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t *smem) {
   using T = typename C::T;
   constexpr int BM = C::BM, MI = C::MI, NI = C::NI, NW = C::NW;
-  constexpr bool A8 = C::LA == Lay::ColK8;
-  constexpr int BOFF = BM * 128;           // B's place in a stage
-  constexpr int UOFF = BOFF + C::BCOLS * 128;  // the second product's B (gated)
-  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
+  using TA = typename TileOf<C::LA, BM, NW>::type;
+  using TB = typename TileOf<C::LB, C::BCOLS, NW>::type;
+  constexpr int BOFF = TA::BYTES;          // B's place in a stage
+  constexpr int UOFF = BOFF + TB::BYTES;   // the second product's B (gated)
+  constexpr int LPS = TA::G + TB::G * (C::GATED ? 2 : 1);  // loads per wave per stage
+  constexpr int KS = kStep / 16;
+  const int t = threadIdx.x, lane = t & 63, wv = wave_id();
   const int wm = wv / C::NWN, wn = wv % C::NWN;
 
-  const int64_t tiles_m = (a.M + BM - 1) / BM;
-  const int64_t tn1 = (a.N + C::OUTN - 1) / C::OUTN, tiles_n = tn1 * a.outs;
-  const int64_t tiles = tiles_m * tiles_n;
+  const int tiles_m = (int)((a.M + BM - 1) / BM);
+  const int tn1 = (int)((a.N + C::OUTN - 1) / C::OUTN), tiles_n = tn1 * a.outs;
+  const uint32_t tiles = (uint32_t)tiles_m * tiles_n;
   const int split = (int)(bid / tiles);
-  int64_t tm, tn;
-  tile_of_block(bid % tiles, tiles_m, tiles_n, tm, tn);
+  int tm, tn;
+  tile_at(bid % tiles, tiles_m, tiles_n, tm, tn);
   const int out = tn >= tn1;
   if (out) tn -= tn1;
-  const int64_t m0 = tm * BM, n0 = tn * C::OUTN;
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * C::OUTN;
 
   // first element of the tile in each operand (of each segment or product)
   const uint8_t *pa[2], *pb[2];
-  constexpr int ea = A8 ? 1 : 2;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    pa[i] = (const uint8_t *)a.a[i] + (C::LA == Lay::RowK ? m0 * a.lda : m0) * ea;
+    pa[i] = (const uint8_t *)a.a[i] + (C::LA == Lay::RowK ? m0 * a.lda : m0) * 2;
     const void *b = a.outs == 2 ? (out ? a.b[1] : a.b[0]) : a.b[i];
     pb[i] = (const uint8_t *)b + (C::LB == Lay::RowK ? n0 * a.ldb : n0) * 2;
   }
 
-  typename TileOf<T, C::LA, BM, NW>::type A;
-  typename TileOf<T, C::LB, C::BCOLS, NW>::type B;
+  TA A;
+  TB B;
   A.init(a.lda, a.M - m0, a.K);
   B.init(a.ldb, a.N - n0, a.K);
 
@@ -352,77 +331,110 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, int64_t bid, uint8_t 
 #pragma unroll
   for (int i = 0; i < MI * NI; ++i) acc[i] = (f32x16){};
 
-  const int64_t n1 = (a.K + kStep - 1) / kStep, nst = n1 * a.segs;
-  const int64_t s0 = nst * split / a.ksplit, s1 = nst * (split + 1) / a.ksplit;
+  const int n1 = (int)((a.K + kStep - 1) / kStep), nst = n1 * a.segs;
+  const int s0 = part_begin(nst, split, a.ksplit), s1 = part_begin(nst, split + 1, a.ksplit);
 
-  // direct-to-LDS loads of stage s, half h of them (0, 1; 2: both)
-  auto load = [&](int64_t s, int h) {
-    const int seg = s >= n1;
-    const int64_t k = (s - (seg ? n1 : 0)) * kStep;
-    uint8_t *buf = smem + ((s - s0) & 1) * C::STAGE;
-    if constexpr (!A8) {
-      constexpr int G = decltype(A)::G;
-      A.load(seg ? pa[1] : pa[0], a.K, a.lda, buf, k, h == 1 ? G / 2 : 0, h == 0 ? G / 2 : G);
-    }
-    constexpr int G = decltype(B)::G;
-    const int j0 = h == 1 ? G / 2 : 0, j1 = h == 0 ? G / 2 : G;
-    if constexpr (C::GATED) {
-      B.load(pb[0], a.K, a.ldb, buf + BOFF, k, j0, j1);
-      B.load(pb[1], a.K, a.ldb, buf + UOFF, k, j0, j1);
+  // The loads of one stage: set up once, then issued one at a time. Past the last
+  // stage every address is out of range, and the loads only write zeros to a
+  // slot that nothing reads: the loop needs no branch for its end.
+  struct Loads {
+    typename TA::Stage a;
+    typename TB::Stage b, u;
+  };
+  auto loads_of = [&](int s) {
+    const int seg = s >= n1 && a.segs > 1;
+    const int k = (s - (seg ? n1 : 0)) * kStep, len = s < s1 ? (int)a.K : 0;
+    const uint8_t *b0 = seg ? pb[1] : pb[0];
+    return Loads{A.stage(seg ? pa[1] : pa[0], a.lda, k, len), B.stage(b0, a.ldb, k, len),
+                 C::GATED ? B.stage(pb[1], a.ldb, k, len) : B.stage(b0, a.ldb, k, len)};
+  };
+  auto load = [&](const Loads &l, uint8_t *buf, int j) {
+    if (j < TA::G)
+      A.load(l.a, buf, j);
+    else if (C::GATED && j >= TA::G + TB::G)
+      B.load(l.u, buf + UOFF, j - TA::G - TB::G);
+    else
+      B.load(l.b, buf + BOFF, j - TA::G);
+  };
+  // the f-th fragment of step ks, in the order in which the MFMAs take them:
+  // b0 a0 b1 a1 a2 a3
+  s16x8 av[2][MI], bv[2][NI];
+  constexpr int FR = MI + NI;
+  auto frag = [&](const uint8_t *cur, int ks, int f) {
+    const int b = ks & 1;
+    if (f == 0 || f == 2) {
+      const int ni = f / 2;
+      bv[b][ni] = C::GATED ? TB::frag(cur + (ni ? UOFF : BOFF), wn * 32, ks, lane)
+                           : TB::frag(cur + BOFF, wn * C::WN + ni * 32, ks, lane);
     } else {
-      B.load(seg ? pb[1] : pb[0], a.K, a.ldb, buf + BOFF, k, j0, j1);
+      const int mi = f == 1 ? 0 : f - 2;
+      av[b][mi] = TA::frag(cur, wm * C::WM + mi * 32, ks, lane);
     }
   };
-  auto fetch = [&](int64_t s) {
-    if constexpr (A8)
-      A.fetch(pa[0], a.lda, a.as + m0 / kCkptBlock, a.ldas, a.K, s * kStep);
+  // The MFMAs of step ks, hook(i) after the i-th: one wave's LDS reads and loads
+  // go out a few at a time between its MFMAs.
+  auto step = [&](int ks, auto hook) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) {
+        acc[mi * NI + ni] = T::mfma32(bv[ks & 1][ni], av[ks & 1][mi], acc[mi * NI + ni]);
+        hook(mi * NI + ni);
+        __builtin_amdgcn_sched_barrier(0);
+      }
   };
-  auto commit = [&](int64_t s) {
-    if constexpr (A8) A.commit(smem + ((s - s0) & 1) * C::STAGE);
+  // All loads and LDS reads of this wave are done, then those of the others.
+  auto ring_sync = [&] {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
 
+  // The k loop. The fragments of a step of 16 are read while the MFMAs of the
+  // step before run, also across stages: once a wave holds the last fragments of
+  // stage s it meets the others, which frees the stage's slot for stage s + 2 and
+  // shows stage s + 1, and runs the last step's MFMAs with the first fragments of
+  // s + 1 and half of the loads of s + 2 between them; the other half goes out
+  // during the next step.
   if (s0 < s1) {
-    fetch(s0);
-    load(s0, 2);
-    commit(s0);
-  }
-  for (int64_t s = s0; s < s1; ++s) {
-    // Stage s has landed for this wave, then for all; that also means that
-    // every wave has read the other buffer to the end. The LDS waits cover a
-    // checkpointed A, written by this wave's own stores.
-    wait_vm<0>();
-    if constexpr (A8) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    asm volatile("s_barrier" ::: "memory");
-    const bool more = s + 1 < s1;
-    if (more) {
-      fetch(s + 1);
-      load(s + 1, 0);
+    constexpr int MM = MI * NI, H = LPS / 2;
+    uint8_t *cur = smem, *next = smem + C::STAGE;
+    {
+      const Loads l0 = loads_of(s0);
+#pragma unroll
+      for (int j = 0; j < LPS; ++j) load(l0, cur, j);
     }
-    const uint8_t *cur = smem + ((s - s0) & 1) * C::STAGE;
-    s16x8 av[2][MI], bv[2][NI];
-    auto frags = [&](int ks, int b) {
+    ring_sync();
+    Loads l = loads_of(s0 + 1);
 #pragma unroll
-      for (int mi = 0; mi < MI; ++mi)
-        av[b][mi] = decltype(A)::frag(cur, wm * C::WM + mi * 32, ks, lane);
+    for (int j = 0; j < H; ++j) load(l, next, j);
 #pragma unroll
-      for (int ni = 0; ni < NI; ++ni)
-        bv[b][ni] = C::GATED
-                        ? decltype(B)::frag(cur + (ni ? UOFF : BOFF), wn * 32, ks, lane)
-                        : decltype(B)::frag(cur + BOFF, wn * C::WN + ni * 32, ks, lane);
-    };
-    frags(0, 0);
+    for (int f = 0; f < FR; ++f) frag(cur, 0, f);
+    for (int s = s0; s < s1; ++s) {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      if (ks < 3) frags(ks + 1, (ks + 1) & 1);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int ks = 0; ks < KS - 1; ++ks)
+        step(ks, [&](int i) {
+          // the last fragments of the stage early: the other waves wait for them
+          const int per = ks == KS - 2 ? 2 : 1;
 #pragma unroll
-      for (int mi = 0; mi < MI; ++mi)
+          for (int f = 0; f < FR; ++f)
+            if (f / per == i || (i == MM - 1 && f / per > i)) frag(cur, ks + 1, f);
+          if (ks == 0)
 #pragma unroll
-        for (int ni = 0; ni < NI; ++ni)
-          acc[mi * NI + ni] = T::mfma32(bv[ks & 1][ni], av[ks & 1][mi], acc[mi * NI + ni]);
-      if (ks == 0 && more) load(s + 1, 1);
-      if (ks == 2 && more) commit(s + 1);
-      __builtin_amdgcn_sched_barrier(0);
+            for (int j = 0; j < H; ++j)
+              if (j * MM / H == i) load(l, next, H + j);
+        });
+      ring_sync();
+      l = loads_of(s + 2);
+      step(KS - 1, [&](int i) {
+#pragma unroll
+        for (int f = 0; f < FR; ++f)
+          if (f == i || (i == MM - 1 && f > i)) frag(next, 0, f);
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+          if (j * MM / H == i) load(l, cur, j);
+      });
+      uint8_t *const t = cur;
+      cur = next, next = t;
     }
   }
   __syncthreads();  // the ring is free for the epilogue

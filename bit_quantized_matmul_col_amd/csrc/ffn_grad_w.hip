@@ -1,14 +1,10 @@
-// dW = X^T dZ, and X^T dG and X^T dU side by side in one launch; X in 16 bits or
-// as an 8-bit checkpoint.
+// dW = X^T dZ, and X^T dG and X^T dU side by side in one launch.
 #include "ffn_gemm.hpp"
 
 namespace llmint8 {
 
 hipError_t launch_ffn_grad_w(int dtype, const FfnGemm &a, int tile, hipStream_t s) {
   using namespace ffn;
-  if (a.as)
-    return dtype == LLMINT8_FP16 ? launch_order<Half, Lay::ColK8, Lay::ColK, false>(a, tile, s)
-                                 : launch_order<Bfloat, Lay::ColK8, Lay::ColK, false>(a, tile, s);
   return dtype == LLMINT8_FP16 ? launch_order<Half, Lay::ColK, Lay::ColK, false>(a, tile, s)
                                : launch_order<Bfloat, Lay::ColK, Lay::ColK, false>(a, tile, s);
 }

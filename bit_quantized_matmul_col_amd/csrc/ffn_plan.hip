@@ -19,6 +19,12 @@ int64_t tiles_of(int tile, bool gated, int64_t M, int64_t N, int outs) {
 
 FfnPlan ffn_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int outs) {
   const bool gated = kind == FfnKind::Gated;
+  if (M <= 64 && (gated || kind == FfnKind::Forward)) {
+    const int64_t blocks = (N + 63) / 64, stages = (K + 127) / 128;
+    int64_t s = (kCus + blocks / 2) / blocks;
+    while (s > 1 && stages < 4 * s) --s;
+    return FfnPlan{0, (int)(s < 1 ? 1 : s)};
+  }
   if (tiles_of(256, gated, M, N, outs) >= kCus / 2) return FfnPlan{256, 1};
   return FfnPlan{128, 1};
 }
@@ -32,7 +38,9 @@ hipError_t launch_ffn(FfnKind kind, int dtype, const FfnGemm &args, const FfnPla
   FfnGemm a = args;
   a.ksplit = p.ksplit;
   hipError_t e = hipSuccess;
-  switch (kind) {
+  if (p.tile == 0)
+    e = launch_ffn_skinny(dtype, kind == FfnKind::Gated, a, s);
+  else switch (kind) {
     case FfnKind::Forward: e = launch_ffn_forward(dtype, a, p.tile, s); break;
     case FfnKind::Gated: e = launch_ffn_gated(dtype, a, p.tile, s); break;
     case FfnKind::GradX: e = launch_ffn_grad_x(dtype, a, p.tile, s); break;

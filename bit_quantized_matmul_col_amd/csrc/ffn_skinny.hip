@@ -1,0 +1,220 @@
+// The forward products for few rows (single tokens, decoding batches): the
+// weights are read once and bound everything, so the kernel is built around
+// keeping HBM busy.
+//
+// A block owns 64 output columns (128 bytes of every row of W, a whole line) and
+// up to 64 rows of X. Its waves take 32-step stages of the reduction in turn,
+// each through a ring of its own in LDS that only this wave writes (direct-to-LDS
+// loads) and reads, so the loop has no barrier: a wave waits for its own oldest
+// stage and keeps the others in flight. W is read from LDS transposed, as in
+// ffn_gemm.hpp, into v_mfma_f32_16x16x32 (16 columns by 16 rows a time). The waves'
+// sums meet in LDS in a fixed order, where the epilogue runs on 8 columns of a
+// row per thread; when the columns alone give too few blocks, the reduction is
+// split over blocks as well and launch_ffn_finish joins the parts.
+#include "ffn_gemm.hpp"
+
+namespace llmint8 {
+namespace ffn {
+
+constexpr int kSkStep = 32;   // reduction steps per stage
+constexpr int kSkCols = 64;   // output columns per block
+constexpr int kSkWaves = 4;
+
+template <class T_, bool GATED_, int MT_, int D_>
+struct SkinnyCfg {
+  using T = T_;
+  static constexpr bool GATED = GATED_;
+  static constexpr int MT = MT_, D = D_;  // 16-row tiles; ring depth
+  static constexpr int P = GATED ? 2 : 1;
+  static constexpr int WBYTES = kSkStep * kSkCols * 2;  // one product's W in a stage
+  static constexpr int STAGE = P * WBYTES + MT * 1024;
+  static constexpr int LOADS = STAGE / 1024;
+  static constexpr int REDP = kSkCols + 4;  // fp32 pitch of the joined sums
+  static constexpr int RED = kSkWaves * P * 16 * MT * REDP * 4;
+  static constexpr int RING = kSkWaves * D * STAGE;
+  static constexpr int LDS = RING > RED ? RING : RED;
+};
+
+// 16-byte chunk c of row r of a W stage (8 chunks a row) sits at c ^ wkey(r): the
+// 8 rows x 32 bytes that half a wave reads then cover all banks once.
+__device__ inline int wkey(int r) { return 2 * (((r >> 1) & 1) + 2 * ((r >> 3) & 1)); }
+// the same for the 64-byte rows of an X stage
+__device__ inline int xkey(int r) { return (r >> 2) & 3; }
+
+template <class C>
+__device__ __forceinline__ void skinny_block(const FfnGemm &a, uint8_t *smem) {
+  using T = typename C::T;
+  constexpr int MT = C::MT, P = C::P, D = C::D;
+  const int t = threadIdx.x, lane = t & 63, wv = wave_id();
+  uint8_t *ring = smem + wv * D * C::STAGE;
+
+  const int tiles = (int)((a.N + kSkCols - 1) / kSkCols);
+  const int split = blockIdx.x / tiles;
+  const int64_t n0 = (int64_t)(blockIdx.x % tiles) * kSkCols, m0 = (int64_t)blockIdx.y * (16 * MT);
+  const int nst = (int)((a.K + kSkStep - 1) / kSkStep);
+  const int s0 = part_begin(nst, split, a.ksplit) + wv;
+  const int s1 = part_begin(nst, split + 1, a.ksplit);
+
+  const int64_t rows = a.M - m0 < 16 * MT ? a.M - m0 : 16 * MT;
+  const uint8_t *px = (const uint8_t *)a.a[0] + m0 * a.lda * 2;
+  const int64_t xbytes = ((rows - 1) * a.lda + a.K) * 2;
+  const uint8_t *pw[2] = {(const uint8_t *)a.b[0] + n0 * 2, (const uint8_t *)a.b[1] + n0 * 2};
+
+  int wvoff[4], xvoff[MT];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = 8 * j + lane / 8;
+    wvoff[j] = r * (int)a.ldb * 2 + 16 * ((lane % 8) ^ wkey(r));
+  }
+  const int xc = (lane % 4) ^ xkey(lane / 4);  // the same chunk in every 16-row tile
+#pragma unroll
+  for (int j = 0; j < MT; ++j) xvoff[j] = (16 * j + lane / 4) * (int)a.lda * 2 + 16 * xc;
+
+  auto load = [&](int s, uint8_t *buf) {
+    const int64_t k = (int64_t)s * kSkStep;
+    const int64_t left = a.K - k < kSkStep ? a.K - k : kSkStep;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const rsrc_t rw = make_rsrc(pw[p] + 2 * k * a.ldb, clip31(((left - 1) * a.ldb + a.N - n0) * 2));
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lptr_t)(buf + p * C::WBYTES + j * 1024), 16,
+                                                 wvoff[j], 0, 0, 0);
+    }
+    const rsrc_t rx = make_rsrc(px + 2 * k, clip31(xbytes - 2 * k));
+    const bool in = 8 * xc < left;
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lptr_t)(buf + P * C::WBYTES + j * 1024), 16,
+                                               in ? xvoff[j] : kOob, 0, 0, 0);
+  };
+
+  f32x4 acc[P][4][MT];
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) acc[p][nb][mt] = (f32x4){};
+
+  const int i = lane & 15, g = lane >> 4;
+  // this wave's stages: s0, s0 + 4, ... below s1
+  const int n = s1 > s0 ? (s1 - s0 + kSkWaves - 1) / kSkWaves : 0;
+#pragma unroll
+  for (int q = 0; q < D - 1; ++q)
+    if (q < n) load(s0 + q * kSkWaves, ring + q * C::STAGE);
+  for (int it = 0, slot = 0; it < n; ++it) {
+    const int nx = it + D - 1;
+    int free_slot = slot + D - 1;
+    if (free_slot >= D) free_slot -= D;
+    // the reads of the slot about to be refilled have been consumed
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (nx < n) {
+      load(s0 + nx * kSkWaves, ring + free_slot * C::STAGE);
+      wait_vm<(D - 1) * C::LOADS>();
+    } else {
+      // the tail: wait for everything; the remaining stages have been in flight
+      // together and land together
+      wait_vm<0>();
+    }
+    const uint8_t *buf = ring + slot * C::STAGE;
+    s16x8 xv[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+      xv[mt] = *(const s16x8 *)(buf + P * C::WBYTES + mt * 1024 + i * 64 + 16 * (g ^ xkey(i)));
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb) {
+        const int r = g * 8 + (i >> 2);
+        const uint8_t *w = buf + p * C::WBYTES + 8 * (i & 1);
+        const int c = nb * 2 + ((i & 3) >> 1);
+        const s16x4 lo = read_tr16((tr_ptr_t)(w + r * 128 + 16 * (c ^ wkey(r))));
+        const s16x4 hi = read_tr16((tr_ptr_t)(w + (r + 4) * 128 + 16 * (c ^ wkey(r + 4))));
+        const s16x8 wf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          acc[p][nb][mt] = T::mfma16(wf, xv[mt], acc[p][nb][mt]);
+      }
+    if (++slot == D) slot = 0;
+  }
+
+  // Lane l of an accumulator holds row l % 16, columns 4 (l / 16) .. + 3.
+  __syncthreads();
+  float *red = (float *)smem;
+  constexpr int PLANE = 16 * MT * C::REDP;
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        *(f32x4 *)(red + (wv * P + p) * PLANE + (mt * 16 + i) * C::REDP + nb * 16 + 4 * g) =
+            acc[p][nb][mt];
+  __syncthreads();
+  for (int x = t; x < (int)rows * 8; x += 64 * kSkWaves) {
+    const int m = x / 8, c8 = (x % 8) * 8;
+    const int64_t row = m0 + m, col = n0 + c8;
+    float v[P][8];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      load_f8(red + p * PLANE + m * C::REDP + c8, v[p]);
+#pragma unroll
+      for (int w = 1; w < kSkWaves; ++w) {
+        float o[8];
+        load_f8(red + (w * P + p) * PLANE + m * C::REDP + c8, o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[p][e] += o[e];
+      }
+    }
+    const bool in = col < a.N;
+    if (a.ksplit > 1) {
+      if (in)
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          store_f8(a.part + (((int64_t)split * P + p) * a.M + row) * a.N + col, v[p]);
+    } else if constexpr (C::GATED) {
+      finish_gated<T>(a, row, col, in, v[0], v[P - 1]);
+    } else if (in) {
+      finish_forward<T>(a, 0, row, col, v[0]);
+    }
+  }
+}
+
+template <class C>
+__global__ __launch_bounds__(64 * kSkWaves, 1) void k_ffn_skinny(FfnGemm a) {
+  extern __shared__ u32x4 smem_v[];
+  skinny_block<C>(a, (uint8_t *)smem_v);
+}
+
+template <class C>
+hipError_t launch_skinny_cfg(const FfnGemm &a, hipStream_t s) {
+  auto *kern = k_ffn_skinny<C>;
+  hipError_t e = hipFuncSetAttribute((const void *)kern,
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+  if (e != hipSuccess) return e;
+  const int64_t tiles = (a.N + kSkCols - 1) / kSkCols, groups = (a.M + 16 * C::MT - 1) / (16 * C::MT);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * a.ksplit), (unsigned)groups),
+                     dim3(64 * kSkWaves), C::LDS, s, a);
+  return hipGetLastError();
+}
+
+template <class T, bool GATED>
+hipError_t launch_skinny(const FfnGemm &a, hipStream_t s) {
+  if (a.M <= 16) return launch_skinny_cfg<SkinnyCfg<T, GATED, 1, 4>>(a, s);
+  if (a.M <= 32) return launch_skinny_cfg<SkinnyCfg<T, GATED, 2, 4>>(a, s);
+  return launch_skinny_cfg<SkinnyCfg<T, GATED, 4, 3>>(a, s);
+}
+
+}  // namespace ffn
+
+hipError_t launch_ffn_skinny(int dtype, bool gated, const FfnGemm &a, hipStream_t s) {
+  using namespace ffn;
+  if (gated)
+    return dtype == LLMINT8_FP16 ? launch_skinny<Half, true>(a, s)
+                                 : launch_skinny<Bfloat, true>(a, s);
+  return dtype == LLMINT8_FP16 ? launch_skinny<Half, false>(a, s)
+                               : launch_skinny<Bfloat, false>(a, s);
+}
+
+}  // namespace llmint8
