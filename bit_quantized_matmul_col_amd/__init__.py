@@ -541,6 +541,13 @@ def _activation(name: str) -> int:
 
 def _matrix(t, name: str, like: torch.Tensor, shape=None) -> int:
     """The leading dimension of a matrix of like's dtype and device."""
+    # the checks in the order of what a valid call needs; the named errors below
+    if (isinstance(t, torch.Tensor) and t.dtype is like.dtype and t.is_cuda and t.dim() == 2
+            and t.device == like.device):
+        M, N = got = tuple(t.shape)
+        s0, s1 = t.stride()
+        if M and N and (s1 == 1 or N == 1) and (shape is None or got == shape):
+            return s0 if M > 1 else N
     _need(t, name, like.dtype, 2)
     if shape is not None:
         _need_shape(t, name, shape)
@@ -549,17 +556,31 @@ def _matrix(t, name: str, like: torch.Tensor, shape=None) -> int:
     return _ld(t, name)
 
 
-def _out(t, name: str, like: torch.Tensor, shape) -> torch.Tensor:
+def _out(t, name: str, like: torch.Tensor, shape):
+    """(tensor, leading dimension) of an output, allocated here if not given."""
     if t is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
-    _matrix(t, name, like, shape)
-    return t
+        return like.new_empty(shape), shape[1]
+    return t, _matrix(t, name, like, shape)
+
+
+def _raw_stream(t: torch.Tensor) -> int:
+    """torch's current stream of t's device, as the hipStream_t itself."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _new_checkpoint(M: int, K: int, device) -> Checkpoint:
-    codes = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :K]
+    codes = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=device)
+    if K % 16:
+        codes = codes[:, :K]
     return Checkpoint(codes, torch.empty((M, -(-K // CHECKPOINT_BLOCK)), dtype=torch.uint8,
                                          device=device))
+
+
+def _c_checkpoint(c: Checkpoint) -> SavedMatrix:
+    """The C view of a checkpoint from _new_checkpoint."""
+    nb = c.scales.shape[1]
+    return SavedMatrix(c.codes.data_ptr(), (c.codes.shape[1] + 15) // 16 * 16,
+                       c.scales.data_ptr(), nb)
 
 
 def _checkpoint(c, name: str, device, shape=None) -> SavedMatrix:
@@ -573,14 +594,11 @@ def _checkpoint(c, name: str, device, shape=None) -> SavedMatrix:
     _need_shape(scales, f"{name}.scales", (M, -(-K // CHECKPOINT_BLOCK)))
     if codes.device != device or scales.device != device:
         raise ValueError(f"{name} must be on {device}")
+    s0, s1 = codes.stride()
     pad = (K + 15) // 16 * 16
-    ld = codes.stride(0) if M > 1 else pad
-    if (K > 1 and codes.stride(1) != 1) or ld < pad:
+    ld = s0 if M > 1 else pad
+    if (K > 1 and s1 != 1) or ld < pad:
         raise ValueError(f"{name}.codes must have unit stride and rows padded to 16 entries")
-    # the calls read each row of codes to the next multiple of 16
-    held = codes.untyped_storage().nbytes() - codes.storage_offset()
-    if held < (M - 1) * ld + pad:
-        raise ValueError(f"{name}.codes: the last row must be padded to 16 entries")
     return SavedMatrix(codes.data_ptr(), ld, scales.data_ptr(), _ld(scales, f"{name}.scales"))
 
 
@@ -592,13 +610,14 @@ def _saved(t, name: str, like: torch.Tensor, shape) -> SavedMatrix:
                        _matrix(t, name, like, shape), None, 0)
 
 
-def _workspace(workspace, need: int, device):
-    """(pointer, size) of the caller's workspace, or of one allocated here."""
+def _workspace(workspace, need: int, like: torch.Tensor):
+    """(pointer, size, tensor) of the caller's workspace, or of one allocated here."""
     if workspace is None:
         if need == 0:
-            return None, 0
-        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
-    return _ws(workspace)
+            return None, 0, None
+        workspace = torch.empty((need,), dtype=torch.uint8, device=like.device)
+        return workspace.data_ptr(), need, workspace
+    return *_ws(workspace), workspace
 
 
 def llmint8_checkpoint_pack(X: torch.Tensor) -> Checkpoint:
@@ -607,8 +626,8 @@ def llmint8_checkpoint_pack(X: torch.Tensor) -> Checkpoint:
     ldx = _matrix(X, "X", X)
     M, K = X.shape
     c = _new_checkpoint(M, K, X.device)
-    out = _checkpoint(c, "checkpoint", X.device)
-    _check(lib().llmint8_checkpoint_pack(_ptr(X), M, K, ldx, dt, C.byref(out), _stream(X)))
+    _check(lib().llmint8_checkpoint_pack(X.data_ptr(), M, K, ldx, dt, C.byref(_c_checkpoint(c)),
+                                         _raw_stream(X)))
     return c
 
 
@@ -621,11 +640,12 @@ def llmint8_checkpoint_unpack(checkpoint: Checkpoint, dtype=torch.float16, *,
     _need(codes, "checkpoint.codes", torch.int8, 2)
     saved = _checkpoint(checkpoint, "checkpoint", codes.device)
     M, K = codes.shape
-    like = torch.empty((0,), dtype=dtype, device=codes.device) if X is not None else None
-    X = (torch.empty((M, K), dtype=dtype, device=codes.device) if X is None
-         else _out(X, "X", like, (M, K)))
-    _check(lib().llmint8_checkpoint_unpack(C.byref(saved), M, K, _DTYPES[dtype], _ptr(X),
-                                           _ld(X, "X"), _stream(X)))
+    if X is None:
+        X, ldx = torch.empty((M, K), dtype=dtype, device=codes.device), K
+    else:
+        ldx = _matrix(X, "X", torch.empty((0,), dtype=dtype, device=codes.device), (M, K))
+    _check(lib().llmint8_checkpoint_unpack(C.byref(saved), M, K, _DTYPES[dtype], X.data_ptr(), ldx,
+                                           _raw_stream(X)))
     return X
 
 
@@ -645,27 +665,28 @@ def llmint8_matmul(X: torch.Tensor, W: torch.Tensor, *, bias: torch.Tensor | Non
     ldx = _matrix(X, "X", X)
     M, K = X.shape
     ldw = _matrix(W, "W", X)
-    N = W.shape[1]
-    if W.shape[0] != K:
+    kw, N = W.shape
+    if kw != K:
         raise ValueError(f"W must be [{K}, N], got {tuple(W.shape)}")
-    Y = _out(Y, "Y", X, (M, N))
     act = _activation(activation)
+    Y, ldy = _out(Y, "Y", X, (M, N))
     opts = None
     if act or bias is not None or residual is not None or Z is not None:
-        opts = MatmulOpts(struct_size=C.sizeof(MatmulOpts), activation=act)
+        o = MatmulOpts(C.sizeof(MatmulOpts), act)
         if bias is not None:
             _need_vec(bias, "bias", X.dtype, N)
-            opts.bias = bias.data_ptr()
+            o.bias = bias.data_ptr()
         if residual is not None:
-            opts.ldr = _matrix(residual, "residual", X, (M, N))
-            opts.residual = residual.data_ptr()
+            o.ldr = _matrix(residual, "residual", X, (M, N))
+            o.residual = residual.data_ptr()
         if Z is not None:
-            opts.ldz = _matrix(Z, "Z", X, (M, N))
-            opts.Z = Z.data_ptr()
+            o.ldz = _matrix(Z, "Z", X, (M, N))
+            o.Z = Z.data_ptr()
+        opts = C.byref(o)
     L = lib()
-    ws, nb = _workspace(workspace, L.llmint8_matmul_workspace_size(M, K, N), X.device)
-    _check(L.llmint8_matmul(_ptr(X), M, K, ldx, _ptr(W), ldw, N, dt, _ptr(Y), _ld(Y, "Y"),
-                            C.byref(opts) if opts is not None else None, ws, nb, _stream(X)))
+    ws, nb, keep = _workspace(workspace, L.llmint8_matmul_workspace_size(M, K, N), X)
+    _check(L.llmint8_matmul(X.data_ptr(), M, K, ldx, W.data_ptr(), ldw, N, dt, Y.data_ptr(), ldy,
+                            opts, ws, nb, _raw_stream(X)))
     return Y
 
 
@@ -680,8 +701,8 @@ def llmint8_matmul_backward(dY: torch.Tensor, X, W: torch.Tensor | None, *,
     """Gradients of llmint8_matmul from dY [M, N]: (dX [M, K], dW [K, N], dbias fp32 [N]),
     None where not needed (the residual's gradient is dY).
 
-    X [M, K] is the 16-bit input or its Checkpoint (only read for dW, but always needed for
-    its shape unless W is given); W [K, N] is only read for dX; Z [M, N] holds the
+    X [M, K] is the 16-bit input or its Checkpoint, read for dW; W [K, N] is read for dX;
+    either may be None where it is not read, but one of them gives K. Z [M, N] holds the
     pre-activations and is needed unless activation is "none"."""
     dt = _dtype_of(dY, "dY")
     lddy = _matrix(dY, "dY", dY)
@@ -700,24 +721,27 @@ def llmint8_matmul_backward(dY: torch.Tensor, X, W: torch.Tensor | None, *,
         K, ldw = (X[0] if isinstance(X, tuple) else X).shape[1], N
     if need_dW and X is None:
         raise ValueError("dW needs X")
-    saved = _saved(X, "X", dY, (M, K)) if need_dW else None
-    if act != LLMINT8_ACT_NONE and Z is None:
-        raise ValueError("Z is needed with an activation")
-    ldz = _matrix(Z, "Z", dY, (M, N)) if act != LLMINT8_ACT_NONE else 0
-    dX = _out(dX, "dX", dY, (M, K)) if need_dX else None
-    dW = _out(dW, "dW", dY, (K, N)) if need_dW else None
-    if need_dbias and dbias is None:
-        dbias = torch.empty((N,), dtype=torch.float32, device=dY.device)
-    if need_dbias:
-        _need_vec(dbias, "dbias", torch.float32, N)
-    else:
+    if not (need_dX or need_dW or need_dbias):
+        raise ValueError("no gradient is asked for")
+    x = C.byref(_saved(X, "X", dY, (M, K))) if need_dW else None
+    z, ldz = None, 0
+    if act != LLMINT8_ACT_NONE:
+        if Z is None:
+            raise ValueError("Z is needed with an activation")
+        z, ldz = Z.data_ptr(), _matrix(Z, "Z", dY, (M, N))
+    dX, lddx = _out(dX, "dX", dY, (M, K)) if need_dX else (None, 0)
+    dW, lddw = _out(dW, "dW", dY, (K, N)) if need_dW else (None, 0)
+    if not need_dbias:
         dbias = None
+    elif dbias is None:
+        dbias = torch.empty((N,), dtype=torch.float32, device=dY.device)
+    else:
+        _need_vec(dbias, "dbias", torch.float32, N)
     L = lib()
-    ws, nb = _workspace(workspace, L.llmint8_matmul_backward_workspace_size(M, K, N), dY.device)
-    _check(L.llmint8_matmul_backward(
-        _ptr(dY), M, N, lddy, C.byref(saved) if saved is not None else None, K, _ptr(W), ldw,
-        _ptr(Z) if ldz else None, ldz, act, dt, _ptr(dX), _ld(dX, "dX") if need_dX else 0,
-        _ptr(dW), _ld(dW, "dW") if need_dW else 0, _ptr(dbias), ws, nb, _stream(dY)))
+    ws, nb, keep = _workspace(workspace, L.llmint8_matmul_backward_workspace_size(M, K, N), dY)
+    _check(L.llmint8_matmul_backward(dY.data_ptr(), M, N, lddy, x, K, _ptr(W), ldw, z, ldz, act, dt,
+                                     _ptr(dX), lddx, _ptr(dW), lddw, _ptr(dbias), ws, nb,
+                                     _raw_stream(dY)))
     return dX, dW, dbias
 
 
@@ -743,22 +767,24 @@ def llmint8_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, *,
     ldx = _matrix(X, "X", X)
     M, K = X.shape
     ldw = _gate_weights(Wg, Wu, X)
-    N = Wg.shape[1]
-    if Wg.shape[0] != K:
+    kw, N = Wg.shape
+    if kw != K:
         raise ValueError(f"Wg and Wu must be [{K}, N], got {tuple(Wg.shape)}")
     act = _activation(activation)
-    H = _out(H, "H", X, (M, N))
     if save not in ("none", "full", "8bit"):
-        raise ValueError("save is 'none', 'full' or '8bit'")
+        raise ValueError(f"save is 'none', 'full' or '8bit', got {save!r}")
+    H, ldh = _out(H, "H", X, (M, N))
     G = U = g = u = None
-    if save != "none":
-        G, U = (torch.empty((M, N), dtype=X.dtype, device=X.device) if save == "full"
-                else _new_checkpoint(M, N, X.device) for _ in range(2))
-        g, u = C.byref(_saved(G, "G", X, (M, N))), C.byref(_saved(U, "U", X, (M, N)))
+    if save == "full":
+        G, U = X.new_empty((M, N)), X.new_empty((M, N))
+        g, u = (C.byref(SavedMatrix(t.data_ptr(), N, None, 0)) for t in (G, U))
+    elif save == "8bit":
+        G, U = _new_checkpoint(M, N, X.device), _new_checkpoint(M, N, X.device)
+        g, u = C.byref(_c_checkpoint(G)), C.byref(_c_checkpoint(U))
     L = lib()
-    ws, nb = _workspace(workspace, L.llmint8_gated_workspace_size(M, K, N), X.device)
-    _check(L.llmint8_gated(_ptr(X), M, K, ldx, _ptr(Wg), _ptr(Wu), ldw, N, act, dt, _ptr(H),
-                           _ld(H, "H"), g, u, ws, nb, _stream(X)))
+    ws, nb, keep = _workspace(workspace, L.llmint8_gated_workspace_size(M, K, N), X)
+    _check(L.llmint8_gated(X.data_ptr(), M, K, ldx, Wg.data_ptr(), Wu.data_ptr(), ldw, N, act, dt,
+                           H.data_ptr(), ldh, g, u, ws, nb, _raw_stream(X)))
     return H if save == "none" else (H, G, U)
 
 
@@ -782,22 +808,24 @@ def llmint8_gated_backward(dH: torch.Tensor, X, Wg: torch.Tensor, Wu: torch.Tens
     act = _activation(activation)
     if need_dW and X is None:
         raise ValueError("dWg and dWu need X")
+    if not (need_dX or need_dW):
+        raise ValueError("no gradient is asked for")
     if isinstance(G, tuple) != isinstance(U, tuple):
         raise ValueError("G and U are both 16-bit matrices or both Checkpoints")
     x = C.byref(_saved(X, "X", dH, (M, K))) if need_dW else None
     g, u = _saved(G, "G", dH, (M, N)), _saved(U, "U", dH, (M, N))
-    dX = _out(dX, "dX", dH, (M, K)) if need_dX else None
+    dX, lddx = _out(dX, "dX", dH, (M, K)) if need_dX else (None, 0)
+    lddw = 0
     if need_dW:
-        dWg, dWu = _out(dWg, "dWg", dH, (K, N)), _out(dWu, "dWu", dH, (K, N))
-        lddw = _ld(dWg, "dWg")
-        if _ld(dWu, "dWu") != lddw:
+        dWg, lddw = _out(dWg, "dWg", dH, (K, N))
+        dWu, ldu = _out(dWu, "dWu", dH, (K, N))
+        if ldu != lddw:
             raise ValueError("dWg and dWu must have the same row stride")
     else:
-        dWg, dWu, lddw = None, None, 0
+        dWg = dWu = None
     L = lib()
-    ws, nb = _workspace(workspace, L.llmint8_gated_backward_workspace_size(M, K, N), dH.device)
-    _check(L.llmint8_gated_backward(
-        _ptr(dH), M, N, lddh, x, K, _ptr(Wg), _ptr(Wu), ldw, C.byref(g), C.byref(u), act, dt,
-        _ptr(dX), _ld(dX, "dX") if need_dX else 0, _ptr(dWg), _ptr(dWu), lddw, ws, nb,
-        _stream(dH)))
+    ws, nb, keep = _workspace(workspace, L.llmint8_gated_backward_workspace_size(M, K, N), dH)
+    _check(L.llmint8_gated_backward(dH.data_ptr(), M, N, lddh, x, K, Wg.data_ptr(), Wu.data_ptr(),
+                                    ldw, C.byref(g), C.byref(u), act, dt, _ptr(dX), lddx,
+                                    _ptr(dWg), _ptr(dWu), lddw, ws, nb, _raw_stream(dH)))
     return dX, dWg, dWu

@@ -158,8 +158,23 @@ __global__ __launch_bounds__(kThreads) void k_bias_join(const float *part, int64
   if (wv == 0 && n < N) dbias[n] = (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]);
 }
 
-// Joins the partial sums of a split reduction (in the order of the parts) and
-// runs the epilogue.
+// Sums of the parts s0, s0 + 1, ... of 8 columns, in the order of the parts; the
+// loads of four parts are in flight together.
+__device__ inline void join_parts(const float *p, int64_t stride, int parts, float *v) {
+  for (int s = 0; s < parts; s += 4) {
+    float x[4][8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (s + q < parts) load_f8(p + (s + q) * stride, x[q]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (s + q < parts)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += x[q][e];
+  }
+}
+
+// Joins the partial sums of a split reduction and runs the epilogue.
 template <class T, bool GATED>
 __global__ __launch_bounds__(kThreads) void k_ffn_finish(FfnGemm a, int cx_log2) {
   const int64_t plane = a.M * a.N;
@@ -167,19 +182,10 @@ __global__ __launch_bounds__(kThreads) void k_ffn_finish(FfnGemm a, int cx_log2)
   for_rows(cx_log2, a.M, a.N, [&](int64_t i, int64_t n, bool in) {
     float v[8] = {0.f}, u[8] = {0.f};
     if (in) {
-      const int per = GATED ? 2 : a.outs;
+      const int64_t per = (GATED ? 2 : a.outs) * plane;
       const float *p = a.part + (GATED ? 0 : out) * plane + i * a.N + n;
-      for (int s = 0; s < a.ksplit; ++s, p += per * plane) {
-        float x[8];
-        load_f8(p, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += x[e];
-        if constexpr (GATED) {
-          load_f8(p + plane, x);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u[e] += x[e];
-        }
-      }
+      join_parts(p, per, a.ksplit, v);
+      if constexpr (GATED) join_parts(p + plane, per, a.ksplit, u);
     }
     if constexpr (GATED)
       ffn::finish_gated<T>(a, i, n, in, v, u);

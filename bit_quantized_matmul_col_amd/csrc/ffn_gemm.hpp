@@ -126,10 +126,10 @@ struct RowKTile {
                                              st.in ? voff[j] : kOob, 0, 0, 0);
   }
 
-  // Fragment of 32 rows from row0 for reduction steps 16 ks .. 16 ks + 15.
+  // Fragment of 16 rows from row0 for reduction steps 32 ks .. 32 ks + 31.
   __device__ static s16x8 frag(const uint8_t *tile, int row0, int ks, int lane) {
-    const int r = row0 + (lane & 31);
-    return *(const s16x8 *)(tile + r * PITCH + 16 * ((2 * ks + (lane >> 5)) ^ key(r)));
+    const int r = row0 + (lane & 15);
+    return *(const s16x8 *)(tile + r * PITCH + 16 * ((4 * ks + (lane >> 4)) ^ key(r)));
   }
 };
 
@@ -155,8 +155,11 @@ struct ColKTile {
   int voff[G];
   int cols;  // columns of the matrix from the tile's first on
 
-  // Rows of 8 chunks: rows r and r + 1 lie in opposite halves of the banks already.
-  __device__ static int key(int r) { return CH >= 16 ? 4 * (r & 3) : 4 * ((r >> 1) & 1); }
+  // Half a wave reads 8 rows (r % 16 in 0 .. 3 and 8 .. 11, or 4 more) x 2 chunks;
+  // rows of 8 chunks lie in opposite halves of the banks by twos already.
+  __device__ static int key(int r) {
+    return CH >= 16 ? 2 * ((r & 3) | (r >> 1 & 4)) : 2 * ((r >> 1 & 1) | (r >> 2 & 2));
+  }
 
   __device__ void init(int64_t ld, int64_t ncols, int64_t) {
     cols = (int)ncols;
@@ -183,11 +186,11 @@ struct ColKTile {
                                              voff[j], 0, 0, 0);
   }
 
+  // Fragment of 16 columns from col0 for reduction steps 32 ks .. 32 ks + 31.
   __device__ static s16x8 frag(const uint8_t *tile, int col0, int ks, int lane) {
-    const int i = lane & 15, g = lane >> 4;
-    const int c = (col0 >> 3) + (g & 1) * 2 + ((i & 3) >> 1);
-    const uint8_t *p = tile + (ks * 16 + (g >> 1) * 8 + (i >> 2)) * PITCH +
-                       16 * (c ^ key(i >> 2)) + 8 * (i & 1);
+    const int i = lane & 15, r = (lane >> 4) * 8 + (i >> 2);
+    const int c = (col0 >> 3) + ((i & 3) >> 1);
+    const uint8_t *p = tile + (ks * 32 + r) * PITCH + 16 * (c ^ key(r)) + 8 * (i & 1);
     const s16x4 lo = read_tr16((tr_ptr_t)p), hi = read_tr16((tr_ptr_t)(p + 4 * PITCH));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   }
@@ -280,14 +283,14 @@ struct Cfg {
   static constexpr bool GATED = GATED_;
   static constexpr int BM = BM_, BN = BN_, NWM = NWM_, NWN = NWN_, NW = NWM * NWN;
   static constexpr int THREADS = 64 * NW;
-  static constexpr int WM = BM / NWM, WN = BN / NWN, MI = WM / 32, NI = WN / 32;
+  static constexpr int WM = BM / NWM, WN = BN / NWN, MI = WM / 16, NI = WN / 16;
   // columns of one output that a block covers, and of its B tile
   static constexpr int OUTN = GATED ? BN / 2 : BN, BCOLS = OUTN;
   static constexpr int STAGE = (BM + BN) * kStep * 2;
   static constexpr int SLABP = WN + 4;  // fp32 pitch of the epilogue's rows
   static constexpr int SLABS = NW * 32 * SLABP * 4;
   static constexpr int LDS = kStages * STAGE > SLABS ? kStages * STAGE : SLABS;
-  static_assert(!GATED || NI == 2, "a gated wave holds 32 columns of each product");
+  static_assert(!GATED || WN == 64, "a gated wave holds 32 columns of each product");
 };
 
 template <class C>
@@ -299,7 +302,6 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
   constexpr int BOFF = TA::BYTES;          // B's place in a stage
   constexpr int UOFF = BOFF + TB::BYTES;   // the second product's B (gated)
   constexpr int LPS = TA::G + TB::G * (C::GATED ? 2 : 1);  // loads per wave per stage
-  constexpr int KS = kStep / 16;
   const int t = threadIdx.x, lane = t & 63, wv = wave_id();
   const int wm = wv / C::NWN, wn = wv % C::NWN;
 
@@ -327,9 +329,9 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
   A.init(a.lda, a.M - m0, a.K);
   B.init(a.ldb, a.N - n0, a.K);
 
-  f32x16 acc[MI * NI];
+  f32x4 acc[MI * NI];
 #pragma unroll
-  for (int i = 0; i < MI * NI; ++i) acc[i] = (f32x16){};
+  for (int i = 0; i < MI * NI; ++i) acc[i] = (f32x4){};
 
   const int n1 = (int)((a.K + kStep - 1) / kStep), nst = n1 * a.segs;
   const int s0 = part_begin(nst, split, a.ksplit), s1 = part_begin(nst, split + 1, a.ksplit);
@@ -356,36 +358,35 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
     else
       B.load(l.b, buf + BOFF, j - TA::G);
   };
-  // the f-th fragment of step ks, in the order in which the MFMAs take them:
-  // b0 a0 b1 a1 a2 a3
+  // the f-th fragment of step ks: B's first, then A's, in the order of the MFMAs
   s16x8 av[2][MI], bv[2][NI];
   constexpr int FR = MI + NI;
   auto frag = [&](const uint8_t *cur, int ks, int f) {
     const int b = ks & 1;
-    if (f == 0 || f == 2) {
-      const int ni = f / 2;
-      bv[b][ni] = C::GATED ? TB::frag(cur + (ni ? UOFF : BOFF), wn * 32, ks, lane)
-                           : TB::frag(cur + BOFF, wn * C::WN + ni * 32, ks, lane);
-    } else {
-      const int mi = f == 1 ? 0 : f - 2;
-      av[b][mi] = TA::frag(cur, wm * C::WM + mi * 32, ks, lane);
-    }
+    if (f < NI)
+      bv[b][f] = C::GATED ? TB::frag(cur + (f >= NI / 2 ? UOFF : BOFF),
+                                     wn * 32 + (f % (NI / 2)) * 16, ks, lane)
+                          : TB::frag(cur + BOFF, wn * C::WN + f * 16, ks, lane);
+    else
+      av[b][f - NI] = TA::frag(cur, wm * C::WM + (f - NI) * 16, ks, lane);
   };
-  // The MFMAs of step ks, hook(i) after the i-th: one wave's LDS reads and loads
-  // go out a few at a time between its MFMAs.
-  auto step = [&](int ks, auto hook) {
+  // MFMAs i0 .. i1 - 1 of step ks, hook(i) after the i-th: a wave's LDS reads and
+  // loads go out one at a time between its MFMAs.
+  constexpr int MM = MI * NI;
+  auto step = [&](int ks, int i0, int i1, auto hook) {
+    __builtin_amdgcn_s_setprio(1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-      for (int ni = 0; ni < NI; ++ni) {
-        acc[mi * NI + ni] = T::mfma32(bv[ks & 1][ni], av[ks & 1][mi], acc[mi * NI + ni]);
-        hook(mi * NI + ni);
+    for (int i = 0; i < MM; ++i)
+      if (i >= i0 && i < i1) {
+        acc[i] = T::mfma16(bv[ks & 1][i % NI], av[ks & 1][i / NI], acc[i]);
+        hook(i);
         __builtin_amdgcn_sched_barrier(0);
       }
   };
   // All loads and LDS reads of this wave are done, then those of the others.
   auto ring_sync = [&] {
+    __builtin_amdgcn_s_setprio(0);
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
 
@@ -396,7 +397,7 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
   // s + 1 and half of the loads of s + 2 between them; the other half goes out
   // during the next step.
   if (s0 < s1) {
-    constexpr int MM = MI * NI, H = LPS / 2;
+    constexpr int H = LPS / 2, Q = MM / 2;  // loads and MFMAs of a quarter stage
     uint8_t *cur = smem, *next = smem + C::STAGE;
     {
       const Loads l0 = loads_of(s0);
@@ -410,28 +411,24 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
 #pragma unroll
     for (int f = 0; f < FR; ++f) frag(cur, 0, f);
     for (int s = s0; s < s1; ++s) {
-#pragma unroll
-      for (int ks = 0; ks < KS - 1; ++ks)
-        step(ks, [&](int i) {
-          // the last fragments of the stage early: the other waves wait for them
-          const int per = ks == KS - 2 ? 2 : 1;
-#pragma unroll
-          for (int f = 0; f < FR; ++f)
-            if (f / per == i || (i == MM - 1 && f / per > i)) frag(cur, ks + 1, f);
-          if (ks == 0)
-#pragma unroll
-            for (int j = 0; j < H; ++j)
-              if (j * MM / H == i) load(l, next, H + j);
-        });
-      ring_sync();
-      l = loads_of(s + 2);
-      step(KS - 1, [&](int i) {
+      step(0, 0, MM, [&](int i) {
 #pragma unroll
         for (int f = 0; f < FR; ++f)
-          if (f == i || (i == MM - 1 && f > i)) frag(next, 0, f);
+          if (f == i) frag(cur, 1, f);
 #pragma unroll
         for (int j = 0; j < H; ++j)
-          if (j * MM / H == i) load(l, cur, j);
+          if (j * Q / H == i) load(l, next, H + j);
+      });
+      step(1, 0, Q, [](int) {});
+      ring_sync();
+      l = loads_of(s + 2);
+      step(1, Q, MM, [&](int i) {
+#pragma unroll
+        for (int f = 0; f < FR; ++f)
+          if (f == i - Q) frag(next, 0, f);
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+          if (j * Q / H == i - Q) load(l, cur, j);
       });
       uint8_t *const t = cur;
       cur = next, next = t;
@@ -439,19 +436,17 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
   }
   __syncthreads();  // the ring is free for the epilogue
 
-  // Lane l of accumulator (mi, ni) holds row l % 32, columns
-  // 8 (r / 4) + 4 (l / 32) + r % 4 of its 32 x 32 block.
+  // Lane l of accumulator (mi, ni) holds row l % 16, columns 4 (l / 16) .. + 3 of
+  // its 16 x 16 block.
   float *slab = (float *)smem + wv * 32 * C::SLABP;
 #pragma unroll
-  for (int mi = 0; mi < MI; ++mi) {
+  for (int mi = 0; mi < MI / 2; ++mi) {
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x16 &c = acc[mi * NI + ni];
-        *(f32x4 *)(slab + (lane & 31) * C::SLABP + ni * 32 + 8 * q + 4 * (lane >> 5)) =
-            f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
-      }
+      for (int ni = 0; ni < NI; ++ni)
+        *(f32x4 *)(slab + (h * 16 + (lane & 15)) * C::SLABP + ni * 16 + 4 * (lane >> 4)) =
+            acc[(2 * mi + h) * NI + ni];
     // the slab is this wave's own: its LDS operations complete in order
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     if constexpr (C::GATED) {

@@ -1,4 +1,24 @@
 // Which kernel a 16-bit product takes.
+//
+// The candidates are square tiles of 256 or 128 rows and columns and, for the
+// forward products of up to kFewMaxM rows, the few-row kernel with 64- or
+// 128-column blocks, each with the reduction whole or split into up to 8 parts.
+// The plan is the candidate with the smallest estimated time. The estimates are
+// sums of a few terms whose constants were fitted to 3200 timed launches on
+// MI355X (bf16; M 1 to 4096, K and N 256 to 28672, every candidate, all four
+// products): they are within 11 % of the measured times (root mean square), and
+// the plans chosen by them cost 1.2 % more than the best candidate (geometric
+// mean over the shapes, 21 % at worst). Some of the choices, in microseconds:
+//   1 x 4096 x 4096       few rows, 64 columns: 4 parts 11.4, whole 13.0
+//   1 x 8192 x 28672      few rows: 128 columns 87.7, 64 columns 105.4
+//   300 x 1040 x 520      few rows 8.0, 128-tiles in 4 parts 11.6
+//   2048 x 4096 x 4096    dX: 128-tiles 62.6, 256-tiles in 2 parts 75.5
+//   2048 x 11008 x 4096   256-tiles: 2 parts 158, whole 212; 128-tiles 171
+//   2048 x 4096 x 11008   gated: 256-tiles 303, 128-tiles 410
+// The plan is a function of the shape alone (the MI355X's 256 CUs, not a device
+// query), so that the workspace queries and the launches agree.
+#include <cmath>
+
 #include "ffn.hpp"
 #include "llmint8.h"
 
@@ -6,27 +26,97 @@ namespace llmint8 {
 
 namespace {
 
-// The plan is a function of the shape alone (the MI355X's 256 CUs, not a device
-// query), so that the workspace queries and the launches agree.
 constexpr int64_t kCus = 256;
+constexpr int64_t kFewMaxM = 384;
 
-int64_t tiles_of(int tile, bool gated, int64_t M, int64_t N, int outs) {
-  const int64_t bn = gated ? tile / 2 : tile;
-  return ((M + tile - 1) / tile) * ((N + bn - 1) / bn) * outs;
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+double mix(double a, double b, double f) { return a + (b - a) * f; }
+
+// Shape of a product: rows and columns of the output(s), reduction length.
+struct Shape {
+  FfnKind kind;
+  int64_t M, N, red;
+  int outs;  // outputs side by side; the gated product has two sums per output
+  bool gated() const { return kind == FfnKind::Gated; }
+  double part_mb(int parts) const {
+    return parts > 1 ? 4e-6 * parts * (gated() ? 2 : outs) * (double)M * (double)N : 0.0;
+  }
+};
+
+int64_t tile_blocks(const Shape &s, int tile, int parts) {
+  return cdiv(s.M, tile) * cdiv(s.N, s.gated() ? tile / 2 : tile) * s.outs * parts;
+}
+
+// Microseconds of a launch of square tiles: rounds of as many blocks as the chip
+// holds (one 256-tile or two 128-tiles per CU), each a number of 64-step stages
+// and an epilogue that take longer the fuller the chip is (clock and memory).
+double tile_us(const Shape &s, int tile, int parts) {
+  const int64_t blocks = tile_blocks(s, tile, parts);
+  double st = (double)cdiv(cdiv(s.red, 64), parts), t;
+  if (tile == 256) {
+    if (s.kind == FfnKind::GradX) st *= 0.89;
+    const double f = (double)(blocks % kCus) / kCus;
+    t = 6.8 + (double)(blocks / kCus) * (st * 1.456 + 7.06);
+    if (f > 0) t += st * mix(1.119, 1.456, f) + mix(2.9, 7.06, f);
+    if (parts > 1) t += 2.8 + 0.261 * s.part_mb(parts);
+  } else {
+    if (s.kind == FfnKind::GradX || s.kind == FfnKind::GradW) st *= 0.755;
+    const double f = (double)(blocks % (2 * kCus)) / kCus;  // blocks per CU of the last round
+    t = 3.73 + (double)(blocks / (2 * kCus)) * (st * 1.12 + 4.15);
+    if (f > 1)
+      t += st * mix(0.867, 1.12, f - 1) + mix(2.56, 4.15, f - 1);
+    else if (f > 0)
+      t += st * mix(0.592, 0.867, f) + mix(0.0, 2.56, f);
+    if (parts > 1) t += 4.2 + 0.23 * s.part_mb(parts);
+  }
+  return t;
+}
+
+// Microseconds of the few-row kernel: what one CU takes for its blocks' bytes and
+// what the whole chip takes for the weights (and for reading them again for
+// further groups of rows), softly the larger of the two.
+double few_us(const Shape &s, int cols, int parts) {
+  const int mt = s.M <= 16 ? 1 : s.M <= 32 ? 2 : 4, p = s.gated() ? 2 : 1;
+  const int64_t groups = cdiv(s.M, 16 * mt), tiles = cdiv(s.N, cols);
+  const double st = (double)cdiv(cdiv(s.red, 128), parts);
+  const double kb = st * 4 * (p * cols * 64 + mt * 1024) * 1e-3;  // per block
+  const double wmb = 2e-6 * (double)s.red * (double)s.N * p;
+  const double xmb = 2e-6 * (double)(tiles * groups * s.red) * 16 * mt + (double)(groups - 1) * wmb;
+  const double cu = kb / 94.4 * (double)cdiv(tiles * groups * parts, kCus) + 0.1;
+  const double chip = wmb / (cols == 64 ? 9.18 : 11.2) + xmb / 45.7;
+  double t = 2.5 + 0.187 * mt * p * cols / 64 +
+             std::pow(std::pow(cu, 0.739) + std::pow(chip, 0.739), 1 / 0.739);
+  if (parts > 1) t += 2.24 + 0.596 * s.part_mb(parts);
+  return 0.9 * t + (parts > 1 ? 1.0 : 0.0);
 }
 
 }  // namespace
 
 FfnPlan ffn_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int outs) {
-  const bool gated = kind == FfnKind::Gated;
-  if (M <= 64 && (gated || kind == FfnKind::Forward)) {
-    const int64_t blocks = (N + 63) / 64, stages = (K + 127) / 128;
-    int64_t s = (kCus + blocks / 2) / blocks;
-    while (s > 1 && stages < 4 * s) --s;
-    return FfnPlan{0, (int)(s < 1 ? 1 : s)};
+  const Shape s{kind, M, N, K * segs, outs};
+  FfnPlan best{false, 256, 1};
+  double best_us = 1e300;
+  auto consider = [&](bool few, int tile, int parts, double us) {
+    if (us < best_us) best = FfnPlan{few, tile, parts}, best_us = us;
+  };
+  const int64_t stages = cdiv(s.red, 64);
+  for (const int parts : {1, 2, 3, 4, 6, 8}) {
+    if (parts > 1 && stages < 3 * parts) break;
+    // more parts than fill the chip once only add partial sums
+    if (parts == 1 || tile_blocks(s, 256, parts) <= kCus)
+      consider(false, 256, parts, tile_us(s, 256, parts));
+    if (parts == 1 || tile_blocks(s, 128, parts) <= 2 * kCus)
+      consider(false, 128, parts, tile_us(s, 128, parts));
+    if ((s.gated() || kind == FfnKind::Forward) && M <= kFewMaxM)
+      for (const int cols : {64, 128}) {
+        // 128-column blocks: one group of rows, whose joined sums fit in LDS
+        if (cols == 128 && M > (s.gated() ? 32 : 64)) continue;
+        if (parts == 1 || cdiv(N, cols) * cdiv(M, 64) * parts <= kCus)
+          consider(true, cols, parts, few_us(s, cols, parts));
+      }
   }
-  if (tiles_of(256, gated, M, N, outs) >= kCus / 2) return FfnPlan{256, 1};
-  return FfnPlan{128, 1};
+  return best;
 }
 
 size_t ffn_part_bytes(const FfnPlan &p, int64_t M, int64_t N, int outs) {
@@ -38,14 +128,16 @@ hipError_t launch_ffn(FfnKind kind, int dtype, const FfnGemm &args, const FfnPla
   FfnGemm a = args;
   a.ksplit = p.ksplit;
   hipError_t e = hipSuccess;
-  if (p.tile == 0)
-    e = launch_ffn_skinny(dtype, kind == FfnKind::Gated, a, s);
-  else switch (kind) {
-    case FfnKind::Forward: e = launch_ffn_forward(dtype, a, p.tile, s); break;
-    case FfnKind::Gated: e = launch_ffn_gated(dtype, a, p.tile, s); break;
-    case FfnKind::GradX: e = launch_ffn_grad_x(dtype, a, p.tile, s); break;
-    case FfnKind::GradW: e = launch_ffn_grad_w(dtype, a, p.tile, s); break;
-  }
+  if (p.few)
+    e = launch_ffn_skinny(dtype, kind == FfnKind::Gated, a, p.tile, s);
+  else if (kind == FfnKind::Forward)
+    e = launch_ffn_forward(dtype, a, p.tile, s);
+  else if (kind == FfnKind::Gated)
+    e = launch_ffn_gated(dtype, a, p.tile, s);
+  else if (kind == FfnKind::GradX)
+    e = launch_ffn_grad_x(dtype, a, p.tile, s);
+  else
+    e = launch_ffn_grad_w(dtype, a, p.tile, s);
   if (e == hipSuccess && p.ksplit > 1)
     e = launch_ffn_finish(dtype, kind == FfnKind::Gated, a, s);
   return e;

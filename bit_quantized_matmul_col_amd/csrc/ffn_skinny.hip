@@ -17,28 +17,28 @@ namespace llmint8 {
 namespace ffn {
 
 constexpr int kSkStep = 32;   // reduction steps per stage
-constexpr int kSkCols = 64;   // output columns per block
 constexpr int kSkWaves = 4;
 
-template <class T_, bool GATED_, int MT_, int D_>
+template <class T_, bool GATED_, int MT_, int CB_>
 struct SkinnyCfg {
   using T = T_;
   static constexpr bool GATED = GATED_;
-  static constexpr int MT = MT_, D = D_;  // 16-row tiles; ring depth
+  static constexpr int MT = MT_;  // 16-row tiles
+  static constexpr int CB = CB_;  // output columns per block
   static constexpr int P = GATED ? 2 : 1;
-  static constexpr int WBYTES = kSkStep * kSkCols * 2;  // one product's W in a stage
+  static constexpr int WBYTES = kSkStep * CB * 2;  // one product's W in a stage
   static constexpr int STAGE = P * WBYTES + MT * 1024;
   static constexpr int LOADS = STAGE / 1024;
-  static constexpr int REDP = kSkCols + 4;  // fp32 pitch of the joined sums
+  static constexpr int REDP = CB + 4;  // fp32 pitch of the joined sums
   static constexpr int RED = kSkWaves * P * 16 * MT * REDP * 4;
+  // three stages, two where three would not fit in LDS; deeper rings (up to 8
+  // stages) measured the same within 3 %
+  static constexpr int FIT = 160 * 1024 / (kSkWaves * STAGE), D = FIT < 3 ? FIT : 3;
   static constexpr int RING = kSkWaves * D * STAGE;
   static constexpr int LDS = RING > RED ? RING : RED;
 };
 
-// 16-byte chunk c of row r of a W stage (8 chunks a row) sits at c ^ wkey(r): the
-// 8 rows x 32 bytes that half a wave reads then cover all banks once.
-__device__ inline int wkey(int r) { return 2 * (((r >> 1) & 1) + 2 * ((r >> 3) & 1)); }
-// the same for the 64-byte rows of an X stage
+// 16-byte chunk c of row r of an X stage (64-byte rows) sits at c ^ xkey(r)
 __device__ inline int xkey(int r) { return (r >> 2) & 3; }
 
 template <class C>
@@ -48,9 +48,9 @@ __device__ __forceinline__ void skinny_block(const FfnGemm &a, uint8_t *smem) {
   const int t = threadIdx.x, lane = t & 63, wv = wave_id();
   uint8_t *ring = smem + wv * D * C::STAGE;
 
-  const int tiles = (int)((a.N + kSkCols - 1) / kSkCols);
+  const int tiles = (int)((a.N + C::CB - 1) / C::CB);
   const int split = blockIdx.x / tiles;
-  const int64_t n0 = (int64_t)(blockIdx.x % tiles) * kSkCols, m0 = (int64_t)blockIdx.y * (16 * MT);
+  const int64_t n0 = (int64_t)(blockIdx.x % tiles) * C::CB, m0 = (int64_t)blockIdx.y * (16 * MT);
   const int nst = (int)((a.K + kSkStep - 1) / kSkStep);
   const int s0 = part_begin(nst, split, a.ksplit) + wv;
   const int s1 = part_begin(nst, split + 1, a.ksplit);
@@ -60,11 +60,14 @@ __device__ __forceinline__ void skinny_block(const FfnGemm &a, uint8_t *smem) {
   const int64_t xbytes = ((rows - 1) * a.lda + a.K) * 2;
   const uint8_t *pw[2] = {(const uint8_t *)a.b[0] + n0 * 2, (const uint8_t *)a.b[1] + n0 * 2};
 
-  int wvoff[4], xvoff[MT];
+  // W stages in the order of a ColKTile
+  using TW = ColKTile<C::CB, 1>;
+  constexpr int WL = C::WBYTES / 1024, CH = TW::CH, RPI = TW::RPI;
+  int wvoff[WL], xvoff[MT];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = 8 * j + lane / 8;
-    wvoff[j] = r * (int)a.ldb * 2 + 16 * ((lane % 8) ^ wkey(r));
+  for (int j = 0; j < WL; ++j) {
+    const int r = RPI * j + lane / CH;
+    wvoff[j] = r * (int)a.ldb * 2 + 16 * ((lane % CH) ^ TW::key(r));
   }
   const int xc = (lane % 4) ^ xkey(lane / 4);  // the same chunk in every 16-row tile
 #pragma unroll
@@ -77,7 +80,7 @@ __device__ __forceinline__ void skinny_block(const FfnGemm &a, uint8_t *smem) {
     for (int p = 0; p < P; ++p) {
       const rsrc_t rw = make_rsrc(pw[p] + 2 * k * a.ldb, clip31(((left - 1) * a.ldb + a.N - n0) * 2));
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < WL; ++j)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lptr_t)(buf + p * C::WBYTES + j * 1024), 16,
                                                  wvoff[j], 0, 0, 0);
     }
@@ -89,11 +92,12 @@ __device__ __forceinline__ void skinny_block(const FfnGemm &a, uint8_t *smem) {
                                                in ? xvoff[j] : kOob, 0, 0, 0);
   };
 
-  f32x4 acc[P][4][MT];
+  constexpr int NB = C::CB / 16;
+  f32x4 acc[P][NB][MT];
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
-    for (int nb = 0; nb < 4; ++nb)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) acc[p][nb][mt] = (f32x4){};
 
@@ -125,13 +129,8 @@ __device__ __forceinline__ void skinny_block(const FfnGemm &a, uint8_t *smem) {
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int nb = 0; nb < 4; ++nb) {
-        const int r = g * 8 + (i >> 2);
-        const uint8_t *w = buf + p * C::WBYTES + 8 * (i & 1);
-        const int c = nb * 2 + ((i & 3) >> 1);
-        const s16x4 lo = read_tr16((tr_ptr_t)(w + r * 128 + 16 * (c ^ wkey(r))));
-        const s16x4 hi = read_tr16((tr_ptr_t)(w + (r + 4) * 128 + 16 * (c ^ wkey(r + 4))));
-        const s16x8 wf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      for (int nb = 0; nb < NB; ++nb) {
+        const s16x8 wf = TW::frag(buf + p * C::WBYTES, nb * 16, 0, lane);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
           acc[p][nb][mt] = T::mfma16(wf, xv[mt], acc[p][nb][mt]);
@@ -146,14 +145,15 @@ __device__ __forceinline__ void skinny_block(const FfnGemm &a, uint8_t *smem) {
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
-    for (int nb = 0; nb < 4; ++nb)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
         *(f32x4 *)(red + (wv * P + p) * PLANE + (mt * 16 + i) * C::REDP + nb * 16 + 4 * g) =
             acc[p][nb][mt];
   __syncthreads();
-  for (int x = t; x < (int)rows * 8; x += 64 * kSkWaves) {
-    const int m = x / 8, c8 = (x % 8) * 8;
+  constexpr int CPR = C::CB / 8;  // 8-column chunks per row
+  for (int x = t; x < (int)rows * CPR; x += 64 * kSkWaves) {
+    const int m = x / CPR, c8 = (x % CPR) * 8;
     const int64_t row = m0 + m, col = n0 + c8;
     float v[P][8];
 #pragma unroll
@@ -193,28 +193,35 @@ hipError_t launch_skinny_cfg(const FfnGemm &a, hipStream_t s) {
   hipError_t e = hipFuncSetAttribute((const void *)kern,
                                      hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
   if (e != hipSuccess) return e;
-  const int64_t tiles = (a.N + kSkCols - 1) / kSkCols, groups = (a.M + 16 * C::MT - 1) / (16 * C::MT);
+  const int64_t tiles = (a.N + C::CB - 1) / C::CB, groups = (a.M + 16 * C::MT - 1) / (16 * C::MT);
   hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * a.ksplit), (unsigned)groups),
                      dim3(64 * kSkWaves), C::LDS, s, a);
   return hipGetLastError();
 }
 
+template <class T, bool GATED, int MT>
+hipError_t launch_skinny_cols(const FfnGemm &a, int cols, hipStream_t s) {
+  if constexpr (!(GATED && MT == 4))  // whose joined sums would not fit in LDS
+    if (cols == 128) return launch_skinny_cfg<SkinnyCfg<T, GATED, MT, 128>>(a, s);
+  return launch_skinny_cfg<SkinnyCfg<T, GATED, MT, 64>>(a, s);
+}
+
 template <class T, bool GATED>
-hipError_t launch_skinny(const FfnGemm &a, hipStream_t s) {
-  if (a.M <= 16) return launch_skinny_cfg<SkinnyCfg<T, GATED, 1, 4>>(a, s);
-  if (a.M <= 32) return launch_skinny_cfg<SkinnyCfg<T, GATED, 2, 4>>(a, s);
-  return launch_skinny_cfg<SkinnyCfg<T, GATED, 4, 3>>(a, s);
+hipError_t launch_skinny(const FfnGemm &a, int cols, hipStream_t s) {
+  if (a.M <= 16) return launch_skinny_cols<T, GATED, 1>(a, cols, s);
+  if (a.M <= 32) return launch_skinny_cols<T, GATED, 2>(a, cols, s);
+  return launch_skinny_cols<T, GATED, 4>(a, cols, s);
 }
 
 }  // namespace ffn
 
-hipError_t launch_ffn_skinny(int dtype, bool gated, const FfnGemm &a, hipStream_t s) {
+hipError_t launch_ffn_skinny(int dtype, bool gated, const FfnGemm &a, int cols, hipStream_t s) {
   using namespace ffn;
   if (gated)
-    return dtype == LLMINT8_FP16 ? launch_skinny<Half, true>(a, s)
-                                 : launch_skinny<Bfloat, true>(a, s);
-  return dtype == LLMINT8_FP16 ? launch_skinny<Half, false>(a, s)
-                               : launch_skinny<Bfloat, false>(a, s);
+    return dtype == LLMINT8_FP16 ? launch_skinny<Half, true>(a, cols, s)
+                                 : launch_skinny<Bfloat, true>(a, cols, s);
+  return dtype == LLMINT8_FP16 ? launch_skinny<Half, false>(a, cols, s)
+                               : launch_skinny<Bfloat, false>(a, cols, s);
 }
 
 }  // namespace llmint8
