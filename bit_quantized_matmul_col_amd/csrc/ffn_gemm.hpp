@@ -198,16 +198,13 @@ struct ColKTile {
 
 // ---- epilogue -------------------------------------------------------------------------
 
-// 8 consecutive columns of one row: act(v + bias) + residual; the sums v + bias
-// go to z on the way.
+// 8 consecutive columns of one row: act(v + b) + r; the sums v + b go to z on the
+// way. b: the bias of the columns (zeros without one); r: the residual's 16 bytes.
 template <class T>
-__device__ inline void finish_forward(const FfnGemm &a, int out, int64_t i, int64_t n, float *v) {
-  if (a.bias) {
-    float b[8];
-    load8<T>(a.bias + n, b);
+__device__ inline void finish_forward(const FfnGemm &a, int out, int64_t i, int64_t n, float *v,
+                                      const float *b, const u32x4 &r) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += b[e];
-  }
+  for (int e = 0; e < 8; ++e) v[e] += b[e];
   if (a.z[0]) store8<T>((uint16_t *)a.z[0] + i * a.ldz + n, v);
   if (a.act != LLMINT8_ACT_NONE)
     with_act(a.act, [&](auto tag) {
@@ -215,12 +212,22 @@ __device__ inline void finish_forward(const FfnGemm &a, int out, int64_t i, int6
       for (int e = 0; e < 8; ++e) v[e] = act_of<decltype(tag)::value>(v[e]);
     });
   if (a.residual) {
-    float r[8];
-    load8<T>(a.residual + i * a.ldr + n, r);
+    const u16x8 h = __builtin_bit_cast(u16x8, r);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += r[e];
+    for (int e = 0; e < 8; ++e) v[e] += T::to_f(h[e]);
   }
   store8<T>((out ? a.y[1] : a.y[0]) + i * a.ldy + n, v);
+}
+
+template <class T>
+__device__ inline void load_bias(const FfnGemm &a, int64_t n, float *b) {
+  if (a.bias) return load8<T>(a.bias + n, b);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) b[e] = 0.f;
+}
+
+__device__ inline u32x4 load_residual(const FfnGemm &a, int64_t i, int64_t n) {
+  return a.residual ? *(const u32x4 *)(a.residual + i * a.ldr + n) : u32x4{0, 0, 0, 0};
 }
 
 // Saves 8 pre-activations in 16 or 8 bits. The 4 lanes of a block of 32 columns
@@ -290,7 +297,10 @@ struct Cfg {
   static constexpr int SLABP = WN + 4;  // fp32 pitch of the epilogue's rows
   static constexpr int SLABS = NW * 32 * SLABP * 4;
   static constexpr int LDS = kStages * STAGE > SLABS ? kStages * STAGE : SLABS;
-  static_assert(!GATED || WN == 64, "a gated wave holds 32 columns of each product");
+  // waves per SIMD that the registers must leave room for
+  static constexpr int WPE = BM * BN / (NW * 64) > 128 ? 1 : 2;
+  static constexpr int WO = GATED ? WN / 2 : WN;  // output columns of a wave
+  static_assert(WO % 32 == 0, "a wave holds whole checkpoint blocks");
 };
 
 template <class C>
@@ -365,7 +375,7 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
     const int b = ks & 1;
     if (f < NI)
       bv[b][f] = C::GATED ? TB::frag(cur + (f >= NI / 2 ? UOFF : BOFF),
-                                     wn * 32 + (f % (NI / 2)) * 16, ks, lane)
+                                     wn * C::WO + (f % (NI / 2)) * 16, ks, lane)
                           : TB::frag(cur + BOFF, wn * C::WN + f * 16, ks, lane);
     else
       av[b][f - NI] = TA::frag(cur, wm * C::WM + (f - NI) * 16, ks, lane);
@@ -397,6 +407,7 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
   // s + 1 and half of the loads of s + 2 between them; the other half goes out
   // during the next step.
   if (s0 < s1) {
+    static_assert(FR <= MM / 2 && LPS % 2 == 0 && MM % LPS == 0, "reads and loads fit between the MFMAs");
     constexpr int H = LPS / 2, Q = MM / 2;  // loads and MFMAs of a quarter stage
     uint8_t *cur = smem, *next = smem + C::STAGE;
     {
@@ -412,23 +423,16 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
     for (int f = 0; f < FR; ++f) frag(cur, 0, f);
     for (int s = s0; s < s1; ++s) {
       step(0, 0, MM, [&](int i) {
-#pragma unroll
-        for (int f = 0; f < FR; ++f)
-          if (f == i) frag(cur, 1, f);
-#pragma unroll
-        for (int j = 0; j < H; ++j)
-          if (j * Q / H == i) load(l, next, H + j);
+        if (i < FR) frag(cur, 1, i);
+        if (i < Q && i % (Q / H) == 0) load(l, next, H + i / (Q / H));
       });
       step(1, 0, Q, [](int) {});
       ring_sync();
       l = loads_of(s + 2);
       step(1, Q, MM, [&](int i) {
-#pragma unroll
-        for (int f = 0; f < FR; ++f)
-          if (f == i - Q) frag(next, 0, f);
-#pragma unroll
-        for (int j = 0; j < H; ++j)
-          if (j * Q / H == i - Q) load(l, cur, j);
+        i -= Q;
+        if (i < FR) frag(next, 0, i);
+        if (i % (Q / H) == 0) load(l, cur, i / (Q / H));
       });
       uint8_t *const t = cur;
       cur = next, next = t;
@@ -439,8 +443,30 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
   // Lane l of accumulator (mi, ni) holds row l % 16, columns 4 (l / 16) .. + 3 of
   // its 16 x 16 block.
   float *slab = (float *)smem + wv * 32 * C::SLABP;
+  constexpr int CPR = C::WO / 8;          // 8-column chunks per row
+  constexpr int PASSES = 32 * CPR / 64;   // rows of a slab go in so many passes
+  const int64_t n = n0 + wn * C::WO + (lane % CPR) * 8;  // this lane's columns
+  auto row_of = [&](int mi, int p) {
+    return m0 + wm * C::WM + mi * 32 + p * (64 / CPR) + lane / CPR;
+  };
+  // the residual of a slab is loaded while the slab before is finished
+  u32x4 res[2][PASSES];
+  auto prefetch = [&](int mi) {
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const int64_t i = row_of(mi, p);
+      if (i < a.M && n < a.N) res[mi & 1][p] = load_residual(a, i, n);
+    }
+  };
+  float bias[8];
+  if constexpr (!C::GATED) {
+    if (n < a.N) load_bias<T>(a, n, bias);
+    if (a.ksplit == 1) prefetch(0);
+  }
 #pragma unroll
   for (int mi = 0; mi < MI / 2; ++mi) {
+    if constexpr (!C::GATED)
+      if (a.ksplit == 1 && mi + 1 < MI / 2) prefetch(mi + 1);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -449,38 +475,24 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
             acc[(2 * mi + h) * NI + ni];
     // the slab is this wave's own: its LDS operations complete in order
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if constexpr (C::GATED) {
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int r = p * 16 + lane / 4, c8 = (lane % 4) * 8;
-        const int64_t i = m0 + wm * C::WM + mi * 32 + r, n = n0 + wn * 32 + c8;
-        float g[8], u[8];
-        load_f8(slab + r * C::SLABP + c8, g);
-        load_f8(slab + r * C::SLABP + 32 + c8, u);
-        if (a.ksplit > 1) {
-          if (i < a.M && n < a.N) {
-            float *part = a.part + ((int64_t)split * 2 * a.M + i) * a.N + n;
-            store_f8(part, g);
-            store_f8(part + a.M * a.N, u);
-          }
-        } else if (i < a.M) {  // uniform over the 4 lanes of a row's block
-          finish_gated<T>(a, i, n, n < a.N, g, u);
+    for (int p = 0; p < PASSES; ++p) {
+      const int r = p * (64 / CPR) + lane / CPR, c8 = (lane % CPR) * 8;
+      const int64_t i = row_of(mi, p);
+      const bool in = i < a.M && n < a.N;
+      float v[8], u[8];
+      load_f8(slab + r * C::SLABP + c8, v);
+      if constexpr (C::GATED) load_f8(slab + r * C::SLABP + C::WO + c8, u);
+      if (a.ksplit > 1) {
+        if (in) {
+          float *part = a.part + (((int64_t)split * (C::GATED ? 2 : a.outs) + out) * a.M + i) * a.N + n;
+          store_f8(part, v);
+          if constexpr (C::GATED) store_f8(part + a.M * a.N, u);
         }
-      }
-    } else {
-      constexpr int CPR = C::WN / 8;  // 8-column chunks per row
-#pragma unroll
-      for (int p = 0; p < 32 * CPR / 64; ++p) {
-        const int r = p * (64 / CPR) + lane / CPR, c8 = (lane % CPR) * 8;
-        const int64_t i = m0 + wm * C::WM + mi * 32 + r, n = n0 + wn * C::WN + c8;
-        if (i < a.M && n < a.N) {
-          float v[8];
-          load_f8(slab + r * C::SLABP + c8, v);
-          if (a.ksplit > 1)
-            store_f8(a.part + (((int64_t)split * a.outs + out) * a.M + i) * a.N + n, v);
-          else
-            finish_forward<T>(a, out, i, n, v);
-        }
+      } else if constexpr (C::GATED) {
+        if (i < a.M) finish_gated<T>(a, i, n, in, v, u);  // the 4 lanes of a block together
+      } else if (in) {
+        finish_forward<T>(a, out, i, n, v, bias, res[mi & 1][p]);
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -488,7 +500,7 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
 }
 
 template <class C>
-__global__ __launch_bounds__(C::THREADS, 2) void k_ffn_gemm(FfnGemm a) {
+__global__ __launch_bounds__(C::THREADS, C::WPE) void k_ffn_gemm(FfnGemm a) {
   extern __shared__ u32x4 smem_v[];
   ffn_tile<C>(a, blockIdx.x, (uint8_t *)smem_v);
 }

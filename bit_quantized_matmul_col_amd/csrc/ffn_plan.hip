@@ -9,7 +9,8 @@
 // products): they are within 11 % of the measured times (root mean square), and
 // the plans chosen by them cost 1.2 % more than the best candidate (geometric
 // mean over the shapes, 21 % at worst). Some of the choices, in microseconds:
-//   1 x 4096 x 4096       few rows, 64 columns: 4 parts 11.4, whole 13.0
+//   1 x 4096 x 4096       few rows, 64 columns: whole 12.5, 4 parts 11.4 (one by one from
+//                         a host 12.0 against 14.9)
 //   1 x 8192 x 28672      few rows: 128 columns 87.7, 64 columns 105.4
 //   300 x 1040 x 520      few rows 8.0, 128-tiles in 4 parts 11.6
 //   2048 x 4096 x 4096    dX: 128-tiles 62.6, 256-tiles in 2 parts 75.5
@@ -98,6 +99,9 @@ FfnPlan ffn_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int ou
   FfnPlan best{false, 256, 1};
   double best_us = 1e300;
   auto consider = [&](bool few, int tile, int parts, double us) {
+    // a host takes about 15 us for a call of two launches with a workspace and 10
+    // for one launch, and gains nothing from a split that the GPU ends before
+    if (parts > 1 && us < 15.0) us = 15.0;
     if (us < best_us) best = FfnPlan{few, tile, parts}, best_us = us;
   };
   const int64_t stages = cdiv(s.red, 64);

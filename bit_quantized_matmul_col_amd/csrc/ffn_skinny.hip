@@ -176,7 +176,9 @@ __device__ __forceinline__ void skinny_block(const FfnGemm &a, uint8_t *smem) {
     } else if constexpr (C::GATED) {
       finish_gated<T>(a, row, col, in, v[0], v[P - 1]);
     } else if (in) {
-      finish_forward<T>(a, 0, row, col, v[0]);
+      float b[8];
+      load_bias<T>(a, col, b);
+      finish_forward<T>(a, 0, row, col, v[0], b, load_residual(a, row, col));
     }
   }
 }
