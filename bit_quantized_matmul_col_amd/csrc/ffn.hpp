@@ -44,6 +44,18 @@ struct FfnPlan {
   int ksplit;
 };
 
+// 256-tiles run in rounds of one block per CU. Where the last round of a launch
+// would be less than half full, the tile columns from tail_cut() on take tiles of
+// half the rows instead, twice as many blocks that finish in about half the time
+// (the first tile column of the tail; `cols` where there is none).
+constexpr int64_t kFfnCus = 256;
+inline int64_t tail_cut(int64_t rows, int64_t cols, int64_t parts) {
+  const int64_t full = rows * cols / kFfnCus;
+  if (parts > 1 || full == 0 || rows * cols % kFfnCus == 0) return cols;
+  const int64_t cut = full * kFfnCus / rows;
+  return 2 * rows * (cols - cut) <= kFfnCus ? cut : cols;
+}
+
 enum class FfnKind { Forward, Gated, GradX, GradW };
 
 FfnPlan ffn_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int outs);

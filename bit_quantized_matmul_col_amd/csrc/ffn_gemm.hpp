@@ -61,13 +61,17 @@ __device__ inline int part_begin(int n, int split, int parts) {
   return (int)((uint64_t)n * split / (uint32_t)parts);
 }
 
-// Tile of block v: the blocks of one XCD (they are dealt out round robin) take
-// consecutive tiles, in groups of up to 8 tile rows, so that its L2 serves the
-// operand tiles that they share.
-__device__ inline void tile_at(uint32_t bid, uint32_t tiles_m, uint32_t tiles_n, int &tm, int &tn) {
+// Tile and part of block bid. The blocks of one XCD (they are dealt out round
+// robin) take consecutive places in the order parts, groups of up to 8 tile rows,
+// columns, rows of the group, so that an XCD works on few parts and neighbouring
+// tiles and its L2 serves the operands that they share.
+__device__ inline void tile_at(uint32_t bid, uint32_t tiles_m, uint32_t tiles_n, uint32_t parts,
+                               int &tm, int &tn, int &part) {
   constexpr uint32_t X = gemm_detail::kXcds, GM = gemm_detail::kGroupM;
-  const uint32_t nb = tiles_m * tiles_n, x = bid % X, rem = nb % X;
-  const uint32_t v = x * (nb / X) + (x < rem ? x : rem) + bid / X;
+  const uint32_t tiles = tiles_m * tiles_n, nb = tiles * parts, x = bid % X, rem = nb % X;
+  const uint32_t place = x * (nb / X) + (x < rem ? x : rem) + bid / X;
+  part = (int)(place / tiles);
+  const uint32_t v = place % tiles;
   const uint32_t first = v / (GM * tiles_n) * GM, in = v % (GM * tiles_n);
   const uint32_t gm = tiles_m - first < GM ? tiles_m - first : GM;
   tm = (int)(first + in % gm);
@@ -303,8 +307,11 @@ struct Cfg {
   static_assert(WO % 32 == 0, "a wave holds whole checkpoint blocks");
 };
 
+// Block bid of the tiles in tile columns col0 .. col0 + cols - 1 (counted over the
+// outputs side by side).
 template <class C>
-__device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t *smem) {
+__device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, int col0, int cols,
+                                         uint8_t *smem) {
   using T = typename C::T;
   constexpr int BM = C::BM, MI = C::MI, NI = C::NI, NW = C::NW;
   using TA = typename TileOf<C::LA, BM, NW>::type;
@@ -316,11 +323,10 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
   const int wm = wv / C::NWN, wn = wv % C::NWN;
 
   const int tiles_m = (int)((a.M + BM - 1) / BM);
-  const int tn1 = (int)((a.N + C::OUTN - 1) / C::OUTN), tiles_n = tn1 * a.outs;
-  const uint32_t tiles = (uint32_t)tiles_m * tiles_n;
-  const int split = (int)(bid / tiles);
-  int tm, tn;
-  tile_at(bid % tiles, tiles_m, tiles_n, tm, tn);
+  const int tn1 = (int)((a.N + C::OUTN - 1) / C::OUTN);
+  int tm, tn, split;
+  tile_at(bid, tiles_m, cols, a.ksplit, tm, tn, split);
+  tn += col0;
   const int out = tn >= tn1;
   if (out) tn -= tn1;
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * C::OUTN;
@@ -407,7 +413,7 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
   // s + 1 and half of the loads of s + 2 between them; the other half goes out
   // during the next step.
   if (s0 < s1) {
-    static_assert(FR <= MM / 2 && LPS % 2 == 0 && MM % LPS == 0, "reads and loads fit between the MFMAs");
+    static_assert(FR <= MM / 2 && LPS % 2 == 0 && LPS <= MM, "they fit between the MFMAs");
     constexpr int H = LPS / 2, Q = MM / 2;  // loads and MFMAs of a quarter stage
     uint8_t *cur = smem, *next = smem + C::STAGE;
     {
@@ -424,7 +430,7 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
     for (int s = s0; s < s1; ++s) {
       step(0, 0, MM, [&](int i) {
         if (i < FR) frag(cur, 1, i);
-        if (i < Q && i % (Q / H) == 0) load(l, next, H + i / (Q / H));
+        if (i % (Q / H) == 0 && i / (Q / H) < H) load(l, next, H + i / (Q / H));
       });
       step(1, 0, Q, [](int) {});
       ring_sync();
@@ -432,7 +438,7 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
       step(1, Q, MM, [&](int i) {
         i -= Q;
         if (i < FR) frag(next, 0, i);
-        if (i % (Q / H) == 0) load(l, cur, i / (Q / H));
+        if (i % (Q / H) == 0 && i / (Q / H) < H) load(l, cur, i / (Q / H));
       });
       uint8_t *const t = cur;
       cur = next, next = t;
@@ -499,29 +505,43 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, uint8_t
   }
 }
 
-template <class C>
-__global__ __launch_bounds__(C::THREADS, C::WPE) void k_ffn_gemm(FfnGemm a) {
+// The blocks before `blocks1` take the 256-row tiles of the tile columns before
+// `cut`, the others the C2 tiles of the rest (see tail_cut).
+template <class C1, class C2>
+__global__ __launch_bounds__(C1::THREADS, 2) void k_ffn_gemm(FfnGemm a, int cut, int cols,
+                                                            uint32_t blocks1) {
+  static_assert(C1::THREADS == C2::THREADS && C1::OUTN == C2::OUTN, "one launch");
   extern __shared__ u32x4 smem_v[];
-  ffn_tile<C>(a, blockIdx.x, (uint8_t *)smem_v);
+  if (blockIdx.x < blocks1)
+    ffn_tile<C1>(a, blockIdx.x, 0, cut, (uint8_t *)smem_v);
+  else
+    ffn_tile<C2>(a, blockIdx.x - blocks1, cut, cols - cut, (uint8_t *)smem_v);
 }
 
-template <class C>
-hipError_t launch_tile(const FfnGemm &a, hipStream_t stream) {
-  auto *kern = k_ffn_gemm<C>;
-  hipError_t e = hipFuncSetAttribute((const void *)kern,
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+template <class C1, class C2>
+hipError_t launch_tiles(const FfnGemm &a, hipStream_t stream) {
+  auto *kern = k_ffn_gemm<C1, C2>;
+  constexpr int LDS = C1::LDS > C2::LDS ? C1::LDS : C2::LDS;
+  hipError_t e =
+      hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
   if (e != hipSuccess) return e;
-  const int64_t blocks = ((a.M + C::BM - 1) / C::BM) * ((a.N + C::OUTN - 1) / C::OUTN) * a.outs *
-                         a.ksplit;
-  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(C::THREADS), C::LDS, stream, a);
+  const int64_t rows = (a.M + C1::BM - 1) / C1::BM;
+  const int64_t cols = (a.N + C1::OUTN - 1) / C1::OUTN * a.outs;
+  const int64_t cut = C1::BM == C2::BM ? cols : tail_cut(rows, cols, a.ksplit);
+  const int64_t blocks1 = rows * cut * a.ksplit;
+  const int64_t blocks2 = (a.M + C2::BM - 1) / C2::BM * (cols - cut) * a.ksplit;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(blocks1 + blocks2)), dim3(C1::THREADS), LDS, stream, a,
+                     (int)cut, (int)cols, (uint32_t)blocks1);
   return hipGetLastError();
 }
 
 // The two tile shapes of one operand order.
 template <class T, Lay LA, Lay LB, bool GATED>
 hipError_t launch_order(const FfnGemm &a, int tile, hipStream_t stream) {
-  if (tile == 256) return launch_tile<Cfg<T, LA, LB, GATED, 256, 256, 2, 4>>(a, stream);
-  return launch_tile<Cfg<T, LA, LB, GATED, 128, 128, 2, 2>>(a, stream);
+  using Wide = Cfg<T, LA, LB, GATED, 256, 256, 2, 4>;
+  using Tail = Cfg<T, LA, LB, GATED, 128, 256, 2, 4>;
+  using Small = Cfg<T, LA, LB, GATED, 128, 128, 2, 2>;
+  return tile == 256 ? launch_tiles<Wide, Tail>(a, stream) : launch_tiles<Small, Small>(a, stream);
 }
 
 }  // namespace ffn

@@ -27,7 +27,7 @@ namespace llmint8 {
 
 namespace {
 
-constexpr int64_t kCus = 256;
+constexpr int64_t kCus = kFfnCus;
 constexpr int64_t kFewMaxM = 384;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -59,7 +59,9 @@ double tile_us(const Shape &s, int tile, int parts) {
     if (s.kind == FfnKind::GradX) st *= 0.89;
     const double f = (double)(blocks % kCus) / kCus;
     t = 6.8 + (double)(blocks / kCus) * (st * 1.456 + 7.06);
-    if (f > 0) t += st * mix(1.119, 1.456, f) + mix(2.9, 7.06, f);
+    const int64_t rows = cdiv(s.M, 256), cols = blocks / (rows * parts);
+    const double half = tail_cut(rows, cols, parts) < cols ? 0.6 : 1.0;
+    if (f > 0) t += half * (st * mix(1.119, 1.456, f) + mix(2.9, 7.06, f));
     if (parts > 1) t += 2.8 + 0.261 * s.part_mb(parts);
   } else {
     if (s.kind == FfnKind::GradX || s.kind == FfnKind::GradW) st *= 0.755;

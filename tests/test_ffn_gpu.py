@@ -71,7 +71,12 @@ def near(got, want):
 # 256-row tiles; a long reduction over few tiles
 SHAPES = [(1, 8, 8), (1, 1040, 520), (2, 4096, 1032), (7, 72, 24), (16, 256, 128), (17, 264, 136),
           (33, 1000, 72), (64, 2048, 264), (65, 64, 264), (129, 40, 1032), (300, 1040, 520),
-          (300, 4104, 136), (1000, 96, 1096), (2049, 72, 4104)]
+          (300, 4104, 136), (1000, 96, 1096), (2049, 72, 4104),
+          # few rows with 64- and 128-column blocks, whole and split; split 128- and
+          # 256-tiles; 256-tiles with and without a tail of half tiles
+          (5, 11008, 520), (3, 520, 28680), (1, 11008, 4096), (20, 4096, 11008), (40, 4104, 1032),
+          (500, 2056, 1032), (1025, 8200, 2056), (2100, 2056, 4104), (1400, 4104, 4104),
+          (2300, 1032, 8200)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
@@ -135,7 +140,8 @@ def test_gated(lm, M, K, N, dtype):
 
 
 BACK = [(1, 8, 8), (1, 264, 72), (37, 72, 136), (64, 128, 128), (129, 264, 520), (300, 1040, 264),
-        (1000, 40, 1096), (513, 2056, 72), (65, 2304, 3336), (4097, 264, 136)]
+        (1000, 40, 1096), (513, 2056, 72), (65, 2304, 3336), (4097, 264, 136),
+        (1030, 4104, 4104), (2000, 2056, 11008), (520, 4096, 4096), (2304, 8200, 1032)]
 
 
 @pytest.mark.parametrize("M,K,N", BACK)
@@ -362,3 +368,76 @@ def test_graph_replay(lm, M, K, N):
         torch.cuda.synchronize()
         for a, b in zip(other, want):
             assert torch.equal(a, b), rep
+
+
+@pytest.mark.parametrize("name", fo.ACTS[1:])
+def test_gradients_against_differences(lm, name):
+    """The kernels' gradients against central differences of the block's output in 64 bits
+    along random directions of every input: for the loss <D, gated(X) Wd + residual>, the
+    difference quotient at step h is off by at most the third derivative times h^2 / 6, and
+    the gradients by the bounds of their roundings (relu is differenced away from its kink)."""
+    say("differences", name)
+    g = gen(41)
+    M, K, N, dt = 24, 64, 96, F16
+    X, Wg, Wu, D = (rand(g, M, K, dt), rand(g, K, N, dt, 0.2), rand(g, K, N, dt, 0.2),
+                    rand(g, M, N, dt))
+    if name == "relu":  # keep every pre-activation at least 0.02 from the kink
+        G = X.double() @ Wg.double()
+        D = torch.where(G.abs() < 0.02, torch.zeros_like(D), D)
+    H, G, U = lm.llmint8_gated(X, Wg, Wu, activation=name, save="full")
+    grads = lm.llmint8_gated_backward(D, X, Wg, Wu, G, U, activation=name)
+    at = [X.double(), Wg.double(), Wu.double()]
+
+    def loss(x, wg, wu):
+        return (D.double() * fo.act(name, x @ wg) * (x @ wu)).sum()
+    for i, grad in enumerate(grads):
+        V = torch.randn(at[i].shape, generator=g, device="cuda", dtype=torch.float64)
+        V /= V.norm()
+        h = 1e-4
+        up, down = [list(at), list(at)]
+        up[i], down[i] = at[i] + h * V, at[i] - h * V
+        want = float((loss(*up) - loss(*down)) / (2 * h))
+        got = float((grad.double() * V).sum())
+        # V has norm 1: independent relative errors of the gradient's entries (its own
+        # rounding, G and U rounded to 16 bits, dG and dU rounded) stay below 8 u of its
+        # norm, differences below 1e-6 of it
+        assert abs(got - want) <= 8 * fo.U[dt] * float(grad.double().norm()) + 1e-6, (name, i)
+
+
+def test_training_example():
+    """The example runs the operators together. Against the same training in plain fp32: the
+    weights start alike and see the same tokens, and the 8-bit checkpoints and 16-bit gradients
+    move Adam's steps by a few hundredths at random, so the loss stays within 5 % of the first
+    one throughout. The int8 layers agree with the trained block."""
+    say("training example")
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "train_feed_forward.py")
+    spec = importlib.util.spec_from_file_location("train_feed_forward", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    steps, tokens, width, hidden, lr = 40, 256, 128, 352, 2e-3
+    losses, W = ex.train(steps, tokens, width, hidden, lr=lr)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    target, master = ex.setup(width, hidden, BF16, g)
+    target = [w.float() for w in target]
+    params = [w.requires_grad_() for w in master]
+    opt = torch.optim.Adam(params, lr=lr, betas=(0.9, 0.99), eps=1e-8)
+    block = lambda x, w: x + (torch.nn.functional.silu(x @ w[0]) * (x @ w[1])) @ w[2]
+    for step in range(steps):
+        X = torch.randn((tokens, width), generator=g, device="cuda").to(BF16).float()
+        err = block(X, params) - block(X, target)
+        loss = err.square().mean()
+        now = float(loss.detach())
+        assert abs(now - losses[step]) < 0.05 * losses[0], (step, now, losses[step])
+        opt.zero_grad()
+        (err.square().sum() / tokens).backward()
+        opt.step()
+    assert losses[-1] < losses[0]
+    X = rand(gen(5), 3, 128, F16)
+    half = [w.half() for w in W]
+    y16, _ = ex.forward(X, half, keep=False)
+    y8 = ex.serve_int8(X, half)
+    # int8 codes of rows and columns: steps of 1/127 of the largest entry, rounded
+    assert float((y8.float() - y16.float()).norm() / y16.float().norm()) < 0.05
