@@ -50,7 +50,6 @@ using gemm_detail::rsrc_t;
 using gemm_detail::wait_vm;
 
 constexpr int kStep = 64;  // reduction steps per stage
-constexpr int kStages = 2;  // LDS ring
 constexpr int kOob = (int)0x80000000;  // an offset past the end of every resource
 
 // The wave's number in its block, known to be the same for all its lanes.
@@ -77,6 +76,11 @@ __device__ inline void tile_at(uint32_t bid, uint32_t tiles_m, uint32_t tiles_n,
   tm = (int)(first + in % gm);
   tn = (int)(in / gm);
 }
+
+template <int N>
+struct Count {
+  static constexpr int value = N;
+};
 
 enum class Lay { RowK, ColK };
 
@@ -287,7 +291,7 @@ struct TileOf<Lay::ColK, N, NW> {
 };
 
 // One launch shape: operand orders, block tile, waves.
-template <class T_, Lay LA_, Lay LB_, bool GATED_, int BM_, int BN_, int NWM_, int NWN_>
+template <class T_, Lay LA_, Lay LB_, bool GATED_, int BM_, int BN_, int NWM_, int NWN_, int NST_ = 2>
 struct Cfg {
   using T = T_;
   static constexpr Lay LA = LA_, LB = LB_;
@@ -297,10 +301,11 @@ struct Cfg {
   static constexpr int WM = BM / NWM, WN = BN / NWN, MI = WM / 16, NI = WN / 16;
   // columns of one output that a block covers, and of its B tile
   static constexpr int OUTN = GATED ? BN / 2 : BN, BCOLS = OUTN;
+  static constexpr int NST = NST_;  // stages in the LDS ring
   static constexpr int STAGE = (BM + BN) * kStep * 2;
   static constexpr int SLABP = WN + 4;  // fp32 pitch of the epilogue's rows
   static constexpr int SLABS = NW * 32 * SLABP * 4;
-  static constexpr int LDS = kStages * STAGE > SLABS ? kStages * STAGE : SLABS;
+  static constexpr int LDS = NST * STAGE > SLABS ? NST * STAGE : SLABS;
   // waves per SIMD that the registers must leave room for
   static constexpr int WPE = BM * BN / (NW * 64) > 128 ? 1 : 2;
   static constexpr int WO = GATED ? WN / 2 : WN;  // output columns of a wave
@@ -400,48 +405,52 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, int col
         __builtin_amdgcn_sched_barrier(0);
       }
   };
-  // All loads and LDS reads of this wave are done, then those of the others.
-  auto ring_sync = [&] {
+  // This wave's loads but for the last `younger` have landed and its LDS reads are
+  // done, then those of the others. Loads are counted, so every stage issues all
+  // of its loads, also past the end.
+  auto ring_sync = [&](auto younger) {
     __builtin_amdgcn_s_setprio(0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    wait_vm<decltype(younger)::value>();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
 
-  // The k loop. The fragments of a step of 16 are read while the MFMAs of the
-  // step before run, also across stages: once a wave holds the last fragments of
-  // stage s it meets the others, which frees the stage's slot for stage s + 2 and
-  // shows stage s + 1, and runs the last step's MFMAs with the first fragments of
-  // s + 1 and half of the loads of s + 2 between them; the other half goes out
-  // during the next step.
+  // The k loop. The fragments of a step of 32 are read while the MFMAs before run,
+  // also across stages: once a wave holds the last fragments of stage s it meets
+  // the others, which frees the stage's slot for stage s + NST and shows stage
+  // s + 1, and runs the last quarter of the MFMAs with the first fragments of
+  // s + 1 and half of the loads of s + NST between them; the other half goes out
+  // during the next quarter.
   if (s0 < s1) {
     static_assert(FR <= MM / 2 && LPS % 2 == 0 && LPS <= MM, "they fit between the MFMAs");
-    constexpr int H = LPS / 2, Q = MM / 2;  // loads and MFMAs of a quarter stage
-    uint8_t *cur = smem, *next = smem + C::STAGE;
-    {
-      const Loads l0 = loads_of(s0);
+    constexpr int NST = C::NST, H = LPS / 2, Q = MM / 2;  // loads and MFMAs of a quarter stage
+    auto slot = [&](int i) { return smem + i * C::STAGE; };
+    Loads l = loads_of(s0);
 #pragma unroll
-      for (int j = 0; j < LPS; ++j) load(l0, cur, j);
+    for (int q = 0; q < NST; ++q) {
+      if (q) l = loads_of(s0 + q);
+#pragma unroll
+      for (int j = 0; j < (q + 1 < NST ? LPS : H); ++j) load(l, slot(q), j);
     }
-    ring_sync();
-    Loads l = loads_of(s0 + 1);
+    ring_sync(Count<(NST - 2) * LPS + H>());
 #pragma unroll
-    for (int j = 0; j < H; ++j) load(l, next, j);
-#pragma unroll
-    for (int f = 0; f < FR; ++f) frag(cur, 0, f);
+    for (int f = 0; f < FR; ++f) frag(smem, 0, f);
+    int at = 0;  // the slot of stage s
     for (int s = s0; s < s1; ++s) {
+      uint8_t *const cur = slot(at), *const last = slot(at == 0 ? NST - 1 : at - 1);
+      at = at + 1 == NST ? 0 : at + 1;
+      const uint8_t *const next = slot(at);
       step(0, 0, MM, [&](int i) {
         if (i < FR) frag(cur, 1, i);
-        if (i % (Q / H) == 0 && i / (Q / H) < H) load(l, next, H + i / (Q / H));
+        if (i % (Q / H) == 0 && i / (Q / H) < H) load(l, last, H + i / (Q / H));
       });
       step(1, 0, Q, [](int) {});
-      ring_sync();
-      l = loads_of(s + 2);
+      ring_sync(Count<(NST - 2) * LPS>());
+      l = loads_of(s + NST);
       step(1, Q, MM, [&](int i) {
         i -= Q;
         if (i < FR) frag(next, 0, i);
         if (i % (Q / H) == 0 && i / (Q / H) < H) load(l, cur, i / (Q / H));
       });
-      uint8_t *const t = cur;
-      cur = next, next = t;
     }
   }
   __syncthreads();  // the ring is free for the epilogue
@@ -505,17 +514,20 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, int col
   }
 }
 
-// The blocks before `blocks1` take the 256-row tiles of the tile columns before
-// `cut`, the others the C2 tiles of the rest (see tail_cut).
+// The last `blocks1` blocks take the C1 tiles of the tile columns before `cut`, the
+// first ones the C2 tiles of the rest (see tail_cut): with the halves first, the
+// CUs stand at different places of their tiles from then on and their epilogues
+// write at different times (1 to 2 % faster than with the halves last).
 template <class C1, class C2>
 __global__ __launch_bounds__(C1::THREADS, 2) void k_ffn_gemm(FfnGemm a, int cut, int cols,
                                                             uint32_t blocks1) {
   static_assert(C1::THREADS == C2::THREADS && C1::OUTN == C2::OUTN, "one launch");
   extern __shared__ u32x4 smem_v[];
-  if (blockIdx.x < blocks1)
-    ffn_tile<C1>(a, blockIdx.x, 0, cut, (uint8_t *)smem_v);
+  const uint32_t blocks2 = gridDim.x - blocks1;
+  if (blockIdx.x >= blocks2)
+    ffn_tile<C1>(a, blockIdx.x - blocks2, 0, cut, (uint8_t *)smem_v);
   else
-    ffn_tile<C2>(a, blockIdx.x - blocks1, cut, cols - cut, (uint8_t *)smem_v);
+    ffn_tile<C2>(a, blockIdx.x, cut, cols - cut, (uint8_t *)smem_v);
 }
 
 template <class C1, class C2>
@@ -535,13 +547,21 @@ hipError_t launch_tiles(const FfnGemm &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The two tile shapes of one operand order.
+// The tile shapes of one operand order. With at most one 128-tile per CU a ring of
+// four stages covers the latency that the second block of the CU covers otherwise
+// (256 x 4096 x 4096 in 4 parts 27.3 -> 23.3 us, whole 49 -> 38; gated
+// 192 x 4096 x 4096 39.9 -> 33.0).
 template <class T, Lay LA, Lay LB, bool GATED>
 hipError_t launch_order(const FfnGemm &a, int tile, hipStream_t stream) {
   using Wide = Cfg<T, LA, LB, GATED, 256, 256, 2, 4>;
   using Tail = Cfg<T, LA, LB, GATED, 128, 256, 2, 4>;
   using Small = Cfg<T, LA, LB, GATED, 128, 128, 2, 2>;
-  return tile == 256 ? launch_tiles<Wide, Tail>(a, stream) : launch_tiles<Small, Small>(a, stream);
+  using Deep = Cfg<T, LA, LB, GATED, 128, 128, 2, 2, 4>;
+  if (tile == 256) return launch_tiles<Wide, Tail>(a, stream);
+  const int64_t blocks = (a.M + 127) / 128 * ((a.N + Small::OUTN - 1) / Small::OUTN) * a.outs *
+                         a.ksplit;
+  return blocks <= kFfnCus ? launch_tiles<Deep, Deep>(a, stream)
+                           : launch_tiles<Small, Small>(a, stream);
 }
 
 }  // namespace ffn

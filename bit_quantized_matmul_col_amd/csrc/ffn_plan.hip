@@ -4,18 +4,20 @@
 // forward products of up to kFewMaxM rows, the few-row kernel with 64- or
 // 128-column blocks, each with the reduction whole or split into up to 8 parts.
 // The plan is the candidate with the smallest estimated time. The estimates are
-// sums of a few terms whose constants were fitted to 3200 timed launches on
+// sums of a few terms whose constants were fitted to 3850 timed launches on
 // MI355X (bf16; M 1 to 4096, K and N 256 to 28672, every candidate, all four
-// products): they are within 11 % of the measured times (root mean square), and
-// the plans chosen by them cost 1.2 % more than the best candidate (geometric
-// mean over the shapes, 21 % at worst). Some of the choices, in microseconds:
+// products): they are within 7 % (256-tiles), 8 % (128-tiles) and 11 % (few rows)
+// of the measured times (root mean square), and the plans chosen by them cost
+// 0.7 % more than the best candidate (geometric mean over the shapes, 33 % at
+// worst). Some of the choices, in microseconds:
 //   1 x 4096 x 4096       few rows, 64 columns: whole 12.5, 4 parts 11.4 (one by one from
 //                         a host 12.0 against 14.9)
 //   1 x 8192 x 28672      few rows: 128 columns 87.7, 64 columns 105.4
-//   300 x 1040 x 520      few rows 8.0, 128-tiles in 4 parts 11.6
+//   300 x 1040 x 520      few rows 8.0, 128-tiles in 4 parts 11.2
+//   256 x 4096 x 4096     few rows 21.9, 128-tiles in 4 parts 23.3, whole 37.7
 //   2048 x 4096 x 4096    dX: 128-tiles 62.6, 256-tiles in 2 parts 75.5
-//   2048 x 11008 x 4096   256-tiles: 2 parts 158, whole 212; 128-tiles 171
-//   2048 x 4096 x 11008   gated: 256-tiles 303, 128-tiles 410
+//   2048 x 11008 x 4096   256-tiles in 2 parts 158, whole 212; 128-tiles 164
+//   2048 x 4096 x 11008   gated: 256-tiles 293, 128-tiles 410
 // The plan is a function of the shape alone (the MI355X's 256 CUs, not a device
 // query), so that the workspace queries and the launches agree.
 #include <cmath>
@@ -49,36 +51,51 @@ int64_t tile_blocks(const Shape &s, int tile, int parts) {
   return cdiv(s.M, tile) * cdiv(s.N, s.gated() ? tile / 2 : tile) * s.outs * parts;
 }
 
+// Softly the larger of two times.
+double larger(double a, double b, double q) {
+  return std::pow(std::pow(a, q) + std::pow(b, q), 1 / q);
+}
+
 // Microseconds of a launch of square tiles: rounds of as many blocks as the chip
-// holds (one 256-tile or two 128-tiles per CU), each a number of 64-step stages
-// and an epilogue that take longer the fuller the chip is (clock and memory).
+// holds (one 256-tile or two 128-tiles per CU; up to one 128-tile per CU runs with
+// a deeper ring), each a number of 64-step stages and an epilogue, and not less
+// than reading the operands takes.
 double tile_us(const Shape &s, int tile, int parts) {
   const int64_t blocks = tile_blocks(s, tile, parts);
-  double st = (double)cdiv(cdiv(s.red, 64), parts), t;
+  const double mb = 2e-6 * (double)s.red * ((double)s.M + (double)s.N * (s.gated() ? 2 : s.outs));
+  double st = (double)cdiv(cdiv(s.red, 64), parts), t, floor;
   if (tile == 256) {
-    if (s.kind == FfnKind::GradX) st *= 0.89;
+    st *= s.kind == FfnKind::GradX ? 0.911 : s.kind == FfnKind::GradW ? 1.046 : 1.0;
     const double f = (double)(blocks % kCus) / kCus;
-    t = 6.8 + (double)(blocks / kCus) * (st * 1.456 + 7.06);
     const int64_t rows = cdiv(s.M, 256), cols = blocks / (rows * parts);
-    const double half = tail_cut(rows, cols, parts) < cols ? 0.6 : 1.0;
-    if (f > 0) t += half * (st * mix(1.119, 1.456, f) + mix(2.9, 7.06, f));
-    if (parts > 1) t += 2.8 + 0.261 * s.part_mb(parts);
+    const double half = tail_cut(rows, cols, parts) < cols ? 0.68 : 1.0;
+    t = 2.59 + (double)(blocks / kCus) * (st * 1.371 + 9.31);
+    if (f > 0) t += half * (st * mix(1.139, 1.371, f) + mix(6.7, 9.31, f));
+    if (parts > 1) t += 1.21 + 0.302 * s.part_mb(parts);
+    floor = 2.59 + mb / 4.02;
   } else {
-    if (s.kind == FfnKind::GradX || s.kind == FfnKind::GradW) st *= 0.755;
-    const double f = (double)(blocks % (2 * kCus)) / kCus;  // blocks per CU of the last round
-    t = 3.73 + (double)(blocks / (2 * kCus)) * (st * 1.12 + 4.15);
-    if (f > 1)
-      t += st * mix(0.867, 1.12, f - 1) + mix(2.56, 4.15, f - 1);
-    else if (f > 0)
-      t += st * mix(0.592, 0.867, f) + mix(0.0, 2.56, f);
-    if (parts > 1) t += 4.2 + 0.23 * s.part_mb(parts);
+    st *= s.kind == FfnKind::GradX ? 0.88 : s.kind == FfnKind::GradW ? 1.042 : 1.0;
+    t = 2.06;
+    if (blocks <= kCus) {
+      const double f = (double)blocks / kCus;
+      t += st * mix(0.465, 0.51, f) + mix(3.51, 5.55, f);
+    } else {
+      const double f = (double)(blocks % (2 * kCus)) / kCus;  // blocks per CU of the last round
+      t += (double)(blocks / (2 * kCus)) * (st * 0.863 + 4.43);
+      if (f > 1)
+        t += st * mix(0.739, 0.863, f - 1) + mix(5.55, 4.43, f - 1);
+      else if (f > 0)
+        t += st * mix(0.55, 0.739, f) + mix(3.51, 5.55, f);
+    }
+    if (parts > 1) t += 1.63 + 0.436 * s.part_mb(parts);
+    floor = 2.06 + mb / 4.29;
   }
-  return t;
+  return larger(t, floor, 6);
 }
 
 // Microseconds of the few-row kernel: what one CU takes for its blocks' bytes and
 // what the whole chip takes for the weights (and for reading them again for
-// further groups of rows), softly the larger of the two.
+// further groups of rows).
 double few_us(const Shape &s, int cols, int parts) {
   const int mt = s.M <= 16 ? 1 : s.M <= 32 ? 2 : 4, p = s.gated() ? 2 : 1;
   const int64_t groups = cdiv(s.M, 16 * mt), tiles = cdiv(s.N, cols);
@@ -86,12 +103,11 @@ double few_us(const Shape &s, int cols, int parts) {
   const double kb = st * 4 * (p * cols * 64 + mt * 1024) * 1e-3;  // per block
   const double wmb = 2e-6 * (double)s.red * (double)s.N * p;
   const double xmb = 2e-6 * (double)(tiles * groups * s.red) * 16 * mt + (double)(groups - 1) * wmb;
-  const double cu = kb / 94.4 * (double)cdiv(tiles * groups * parts, kCus) + 0.1;
-  const double chip = wmb / (cols == 64 ? 9.18 : 11.2) + xmb / 45.7;
-  double t = 2.5 + 0.187 * mt * p * cols / 64 +
-             std::pow(std::pow(cu, 0.739) + std::pow(chip, 0.739), 1 / 0.739);
-  if (parts > 1) t += 2.24 + 0.596 * s.part_mb(parts);
-  return 0.9 * t + (parts > 1 ? 1.0 : 0.0);
+  const double cu = kb / (cols == 64 ? 91.0 : 94.7) * (double)cdiv(tiles * groups * parts, kCus);
+  const double chip = wmb / (cols == 64 ? 8.42 : 10.0) + xmb / 63.1;
+  double t = 2.26 + 0.253 * mt * p * cols / 64 + larger(cu, chip, 0.786);
+  if (parts > 1) t += 2.4 + 0.394 * s.part_mb(parts);
+  return t;
 }
 
 }  // namespace
@@ -101,9 +117,10 @@ FfnPlan ffn_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int ou
   FfnPlan best{false, 256, 1};
   double best_us = 1e300;
   auto consider = [&](bool few, int tile, int parts, double us) {
-    // a host takes about 15 us for a call of two launches with a workspace and 10
-    // for one launch, and gains nothing from a split that the GPU ends before
-    if (parts > 1 && us < 15.0) us = 15.0;
+    // A host takes about 15 us for a call of two launches with a workspace and 10
+    // for one launch, and gains nothing from a split that the GPU ends before (16.5:
+    // the estimates of whole few-row launches are up to a quarter high there).
+    if (parts > 1) us = us + 1.0 < 16.5 ? 16.5 : us + 1.0;
     if (us < best_us) best = FfnPlan{few, tile, parts}, best_us = us;
   };
   const int64_t stages = cdiv(s.red, 64);
