@@ -586,6 +586,18 @@ def _c_checkpoint(c: Checkpoint) -> SavedMatrix:
 def _checkpoint(c, name: str, device, shape=None) -> SavedMatrix:
     """The C view of a checkpoint, after checking it."""
     codes, scales = c
+    # as in _matrix, what a valid one needs first
+    if (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor)
+            and codes.dtype is torch.int8 and scales.dtype is torch.uint8
+            and codes.device == device and scales.device == device and codes.is_cuda
+            and codes.dim() == 2):
+        M, K = got = tuple(codes.shape)
+        (s0, s1), blocks = codes.stride(), -(-K // CHECKPOINT_BLOCK)
+        if (M > 1 and K and s1 == 1 and s0 >= (K + 15) // 16 * 16
+                and (shape is None or got == shape) and tuple(scales.shape) == (M, blocks)):
+            t0, t1 = scales.stride()
+            if t1 == 1 or blocks == 1:
+                return SavedMatrix(codes.data_ptr(), s0, scales.data_ptr(), t0)
     _need(codes, f"{name}.codes", torch.int8, 2)
     if shape is not None:
         _need_shape(codes, f"{name}.codes", shape)

@@ -62,6 +62,18 @@ FfnPlan ffn_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int ou
 // bytes of the partial sums of a plan
 size_t ffn_part_bytes(const FfnPlan &p, int64_t M, int64_t N, int outs);
 
+// How a backward pass runs its products: where only one is asked for, by its own
+// plan; both in one launch of square tiles, with the parts of each.
+struct FfnBackPlan {
+  FfnPlan x, w;
+  int tile, xsplit, wsplit;
+};
+// dZ is [M x N], X [M x K]; grads: gradients of one (1) or two (2) products.
+FfnBackPlan ffn_back_plan(int64_t M, int64_t K, int64_t N, int grads);
+hipError_t launch_ffn_together(int dtype, const FfnGemm &x, const FfnGemm &w, const FfnBackPlan &p,
+                               hipStream_t s);
+hipError_t launch_ffn_back(int dtype, const FfnGemm &x, const FfnGemm &w, int tile, hipStream_t s);
+
 // The plan's kernel and, for a split reduction, the pass that joins the parts.
 // dtype: 0 fp16, 1 bf16.
 hipError_t launch_ffn(FfnKind kind, int dtype, const FfnGemm &a, const FfnPlan &p, hipStream_t s);

@@ -67,17 +67,15 @@ Saved saved_of(const llmint8_saved *s) { return Saved{s->data, s->ld, s->scales,
 
 // Workspace of a backward pass: the 16-bit operands of its products (`grads` of
 // them), a checkpointed X expanded to 16 bits, the bias gradient's partial sums,
-// and the partial sums of the split products (one region, the products run one
-// after the other).
+// and the partial sums of the split products, dX's and dW's.
 struct BackLayout {
-  size_t dz, x, bias, part, total;
-  FfnPlan px, pw;
+  size_t dz, x, bias, part_x, part_w, total;
+  FfnBackPlan plan;
 };
 
 BackLayout back_layout(int64_t M, int64_t K, int64_t N, int grads) {
   BackLayout L{};
-  L.px = ffn_plan(FfnKind::GradX, M, K, N, grads, 1);
-  L.pw = ffn_plan(FfnKind::GradW, K, N, M, 1, grads);
+  L.plan = ffn_back_plan(M, K, N, grads);
   size_t o = 0;
   L.dz = o;
   o += up((size_t)grads * M * pitch8(N) * 2);
@@ -85,49 +83,66 @@ BackLayout back_layout(int64_t M, int64_t K, int64_t N, int grads) {
   o += up((size_t)M * K * 2);
   L.bias = o;
   if (grads == 1) o += up((size_t)bias_rows(M, N) * N * 4);
-  L.part = o;
-  const size_t bx = ffn_part_bytes(L.px, M, K, 1), bw = ffn_part_bytes(L.pw, K, N, grads);
-  o += up(bx > bw ? bx : bw);
+  const FfnPlan tx{false, L.plan.tile, L.plan.xsplit}, tw{false, L.plan.tile, L.plan.wsplit};
+  auto room = [](size_t x, size_t y) { return up(x > y ? x : y); };
+  L.part_x = o;
+  o += room(ffn_part_bytes(L.plan.x, M, K, 1), ffn_part_bytes(tx, M, K, 1));
+  L.part_w = o;
+  o += room(ffn_part_bytes(L.plan.w, K, N, grads), ffn_part_bytes(tw, K, N, grads));
   L.total = o;
   return L;
 }
 
-// dX = sum over the segments of dZ_i W_i^T.
-hipError_t grad_x(int dtype, const uint16_t *const *dz, int64_t lddz, const uint16_t *const *w,
-                  int64_t ldw, int segs, int64_t M, int64_t K, int64_t N, uint16_t *dX,
-                  int64_t lddx, const FfnPlan &p, float *part, hipStream_t s) {
-  FfnGemm a{};
-  for (int i = 0; i < segs; ++i) a.a[i] = dz[i], a.b[i] = w[i];
-  a.lda = lddz, a.ldb = ldw;
-  a.M = M, a.N = K, a.K = N;
-  a.segs = segs, a.outs = 1;
-  a.y[0] = dX, a.ldy = lddx;
-  a.part = part;
-  return launch_ffn(FfnKind::GradX, dtype, a, p, s);
-}
+// The products of a backward pass: dX = sum of dZ_i W_i^T and dW_i = X^T dZ_i for
+// `grads` products, either of them only where its outputs are given. A
+// checkpointed X is expanded into the workspace first, exactly: a pass of 3 bytes
+// an entry against a product of 2 N or 4 N operations an entry. Expanding the
+// codes inside the product's tiles instead (8-bit loads to registers, 16-bit
+// stores to LDS) cost more than the pass at 2048 x 4096 x 11008: 438 against
+// 412 + 6 us.
+struct Grads {
+  int count;
+  const uint16_t *dz[2];
+  int64_t lddz;
+  const llmint8_saved *X;
+  const uint16_t *w[2];
+  int64_t ldw;
+  uint16_t *dX;
+  int64_t lddx;
+  uint16_t *dW[2];
+  int64_t lddw;
+};
 
-// dW_i = X^T dZ_i for the outputs side by side. A checkpointed X is expanded into
-// `room` first, exactly: a pass of 3 bytes an entry against a product of 2 N or
-// 4 N operations an entry. Expanding the codes inside the product's tiles instead
-// (8-bit loads to registers, 16-bit stores to LDS) cost more than the pass at
-// 2048 x 4096 x 11008: 438 against 412 + 6 us.
-hipError_t grad_w(int dtype, const llmint8_saved &X, uint16_t *room, const uint16_t *const *dz,
-                  int64_t lddz, int outs, int64_t M, int64_t K, int64_t N, uint16_t *const *dW,
-                  int64_t lddw, const FfnPlan &p, float *part, hipStream_t s) {
-  FfnGemm a{};
-  a.a[0] = X.data, a.lda = X.ld;
-  if (X.scales) {
-    const hipError_t e = launch_ckpt_unpack(dtype, saved_of(&X), M, K, room, K, s);
-    if (e != hipSuccess) return e;
-    a.a[0] = room, a.lda = K;
+hipError_t run_grads(int dtype, const Grads &g, int64_t M, int64_t K, int64_t N, uint8_t *ws,
+                     const BackLayout &L, hipStream_t s) {
+  FfnGemm x{}, w{};
+  if (g.dX) {
+    for (int i = 0; i < g.count; ++i) x.a[i] = g.dz[i], x.b[i] = g.w[i];
+    x.lda = g.lddz, x.ldb = g.ldw;
+    x.M = M, x.N = K, x.K = N;
+    x.segs = g.count, x.outs = 1;
+    x.y[0] = g.dX, x.ldy = g.lddx;
+    x.part = (float *)(ws + L.part_x);
   }
-  for (int i = 0; i < outs; ++i) a.b[i] = dz[i], a.y[i] = dW[i];
-  a.ldb = lddz;
-  a.M = K, a.N = N, a.K = M;
-  a.segs = 1, a.outs = outs;
-  a.ldy = lddw;
-  a.part = part;
-  return launch_ffn(FfnKind::GradW, dtype, a, p, s);
+  if (g.dW[0]) {
+    w.a[0] = g.X->data, w.lda = g.X->ld;
+    if (g.X->scales) {
+      uint16_t *room = (uint16_t *)(ws + L.x);
+      const hipError_t e = launch_ckpt_unpack(dtype, saved_of(g.X), M, K, room, K, s);
+      if (e != hipSuccess) return e;
+      w.a[0] = room, w.lda = K;
+    }
+    for (int i = 0; i < g.count; ++i) w.b[i] = g.dz[i], w.y[i] = g.dW[i];
+    w.ldb = g.lddz;
+    w.M = K, w.N = N, w.K = M;
+    w.segs = 1, w.outs = g.count;
+    w.ldy = g.lddw;
+    w.part = (float *)(ws + L.part_w);
+  }
+  if (g.dX && g.dW[0]) return launch_ffn_together(dtype, x, w, L.plan, s);
+  hipError_t e = g.dX ? launch_ffn(FfnKind::GradX, dtype, x, L.plan.x, s) : hipSuccess;
+  if (e == hipSuccess && g.dW[0]) e = launch_ffn(FfnKind::GradW, dtype, w, L.plan.w, s);
+  return e;
 }
 
 }  // namespace
@@ -224,14 +239,13 @@ LLMINT8_EXPORT int llmint8_matmul_backward(const uint16_t *dY, int64_t M, int64_
   uint16_t *own = (uint16_t *)(ws + L.dz);
   const uint16_t *dz = act ? own : dY;
   const int64_t lddz = act ? pitch8(N) : lddy;
-  float *part = (float *)(ws + L.part);
   hipError_t e = hipSuccess;
   if (act || dbias)
     e = launch_act_grad(dtype, activation, dY, lddy, Z, ldz, M, N, act && products ? own : nullptr,
                         lddz, dbias, (float *)(ws + L.bias), s);
-  if (e == hipSuccess && dX)
-    e = grad_x(dtype, &dz, lddz, &W, ldw, 1, M, K, N, dX, lddx, L.px, part, s);
-  if (e == hipSuccess && dW) e = grad_w(dtype, *X, (uint16_t *)(ws + L.x), &dz, lddz, 1, M, K, N, &dW, lddw, L.pw, part, s);
+  if (e == hipSuccess && products)
+    e = run_grads(dtype, Grads{1, {dz, nullptr}, lddz, X, {W, nullptr}, ldw, dX, lddx,
+                               {dW, nullptr}, lddw}, M, K, N, ws, L, s);
   return hip_status(e);
 }
 
@@ -306,13 +320,10 @@ LLMINT8_EXPORT int llmint8_gated_backward(const uint16_t *dH, int64_t M, int64_t
   uint8_t *ws = (uint8_t *)workspace;
   const int64_t lddz = pitch8(N);
   uint16_t *dg = (uint16_t *)(ws + L.dz), *du = dg + M * lddz;
-  float *part = (float *)(ws + L.part);
-  const uint16_t *dz[2] = {dg, du}, *w[2] = {Wg, Wu};
-  uint16_t *dw[2] = {dWg, dWu};
   hipError_t e = launch_gated_grad(dtype, activation, dH, lddh, saved_of(G), saved_of(U), M, N, dg,
                                    du, lddz, s);
-  if (e == hipSuccess && dX)
-    e = grad_x(dtype, dz, lddz, w, ldw, 2, M, K, N, dX, lddx, L.px, part, s);
-  if (e == hipSuccess && dWg) e = grad_w(dtype, *X, (uint16_t *)(ws + L.x), dz, lddz, 2, M, K, N, dw, lddw, L.pw, part, s);
+  if (e == hipSuccess)
+    e = run_grads(dtype, Grads{2, {dg, du}, lddz, X, {Wg, Wu}, ldw, dX, lddx, {dWg, dWu}, lddw}, M,
+                  K, N, ws, L, s);
   return hip_status(e);
 }
