@@ -186,8 +186,9 @@ struct ColKTile {
   };
   __device__ Stage stage(const uint8_t *mat, int64_t ld, int k, int len) const {
     const int left = len - k, rows = left < kStep ? left : kStep;
-    const int n = ((rows - 1) * (int)ld + cols) * 2;
-    return Stage{make_rsrc(mat + 2 * (int64_t)k * ld, n > 0 ? n : 0)};
+    // (with `left` below 1 the product could wrap)
+    const int n = left > 0 ? ((rows - 1) * (int)ld + cols) * 2 : 0;
+    return Stage{make_rsrc(mat + 2 * (int64_t)k * ld, n)};
   }
   __device__ void load(const Stage &st, uint8_t *to, int j) const {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rs, (lptr_t)(to + (wave_id() + NW * j) * 1024), 16,
@@ -453,6 +454,7 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, int col
       });
     }
   }
+  wait_vm<0>();     // this wave's loads past the end
   __syncthreads();  // the ring is free for the epilogue
 
   // Lane l of accumulator (mi, ni) holds row l % 16, columns 4 (l / 16) .. + 3 of

@@ -101,6 +101,36 @@ def test_matmul(lm, M, K, N, dtype):
     near(a, fo.matmul(X.double(), W.double(), None, None, "none", dtype)[0])
 
 
+def test_rows_more_than_2_gib_apart(lm):
+    """Row strides of 2 MiB: byte offsets pass 31 and 32 bits, also those of the stages that
+    the loop asks for past the end of the reduction."""
+    pitch, n = 1 << 20, 72
+    base = torch.empty((2200, pitch), dtype=BF16, device="cuda")
+    g = gen(3)
+
+    def wide(rows, column):
+        v = base[:rows, column:column + n]
+        v.copy_(rand(g, rows, n, BF16))
+        return v
+
+    for M, K in ((5, 2192), (400, 1104), (400, 2192)):
+        say("wide strides, forward", M, K)
+        X, W, Wu = rand(g, M, K, BF16, 0.05), wide(K, 0), wide(K, 512)
+        near(lm.llmint8_matmul(X, W), fo.matmul(X.double(), W.double(), None, None, "none", BF16)[0])
+        h, dh = fo.gated(X.double(), W.double(), Wu.double(), "silu", BF16)[0]
+        near(lm.llmint8_gated(X, W, Wu), (h, dh))
+    for M in (1103, 2200):
+        say("wide strides, backward", M)
+        dY, X, W = wide(M, 0), wide(M, 512), rand(g, n, n, BF16)
+        dX, dW, _ = lm.llmint8_matmul_backward(dY, X, W)
+        alone = lm.llmint8_matmul_backward(dY, X, W, need_dX=False)[1]
+        wx = fo.product(dY.double(), W.double().t())
+        ww = fo.product(X.double().t(), dY.double())
+        near(dX, (wx[0], fo.stored(*wx, BF16)))
+        near(dW, (ww[0], fo.stored(*ww, BF16)))
+        near(alone, (ww[0], fo.stored(*ww, BF16)))
+
+
 @pytest.mark.parametrize("name", fo.ACTS)
 @pytest.mark.parametrize("M", [5, 200])
 def test_matmul_activations(lm, name, M):
