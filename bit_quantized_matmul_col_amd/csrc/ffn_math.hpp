@@ -16,10 +16,6 @@ struct Half {
   typedef _Float16 elem;
   __device__ static float to_f(uint16_t u) { return (float)__builtin_bit_cast(_Float16, u); }
   __device__ static uint16_t from_f(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
-  __device__ static f32x16 mfma32(s16x8 a, s16x8 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
-                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-  }
   __device__ static f32x4 mfma16(s16x8 a, s16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -30,10 +26,6 @@ struct Bfloat {
   typedef __bf16 elem;
   __device__ static float to_f(uint16_t u) { return __builtin_bit_cast(float, (uint32_t)u << 16); }
   __device__ static uint16_t from_f(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
-  __device__ static f32x16 mfma32(s16x8 a, s16x8 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  }
   __device__ static f32x4 mfma16(s16x8 a, s16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -77,8 +69,8 @@ __device__ inline float erf_of(float x) {
 }
 
 // act(z) and act'(z). gelu_tanh: (1 + tanh v) / 2 is the logistic of 2v. A NaN
-// stays NaN; where a formula is 0 * infinity (silu and gelu at -infinity), so is
-// the result NaN.
+// stays NaN (relu' is z > 0, 0 at a NaN); where a formula is 0 * infinity (silu and
+// gelu at -infinity), so is the result NaN.
 template <int ACT>
 __device__ inline float act_of(float z) {
   if constexpr (ACT == LLMINT8_ACT_RELU) return z > 0.f ? z : (z == z ? 0.f : z);

@@ -317,8 +317,7 @@ int llmint8_linear_fp8(const uint16_t *X, int64_t M, int64_t K, int64_t ldx,
  * held as the byte e + 127; code = clamp(rint(x 2^-e), -127, 127), ties to
  * even, and the entry stands for code 2^e. That value is exact in fp16 and bf16.
  * A block that holds an infinity or a NaN takes the byte 255 and stands for NaN.
- *   data     codes [M x ld], ld a multiple of 16; calls read rows up to the
- *            next multiple of 16 entries.
+ *   data     codes [M x ld], ld a multiple of 16.
  *   scales   [M x ld_scales] bytes, ld_scales >= ceil(columns / 32).
  */
 typedef struct llmint8_saved {
