@@ -36,12 +36,13 @@ struct FfnGemm {
 };
 
 // Which kernel a product takes: square tiles of `tile` rows and columns (256 or
-// 128), or the kernel for few rows with blocks of `tile` columns (64 or 128); and
-// in how many parts the reduction is split.
+// 128), or the kernel for few rows with blocks of `tile` columns (32, 64 or 128) and
+// `rows` rows (16, 32 or 64); and in how many parts the reduction is split.
 struct FfnPlan {
   bool few;
   int tile;
   int ksplit;
+  int rows;
 };
 
 // 256-tiles run in rounds of one block per CU. Where the last round of a launch
@@ -82,7 +83,8 @@ hipError_t launch_ffn_forward(int dtype, const FfnGemm &a, int tile, hipStream_t
 hipError_t launch_ffn_gated(int dtype, const FfnGemm &a, int tile, hipStream_t s);
 hipError_t launch_ffn_grad_x(int dtype, const FfnGemm &a, int tile, hipStream_t s);
 hipError_t launch_ffn_grad_w(int dtype, const FfnGemm &a, int tile, hipStream_t s);
-hipError_t launch_ffn_skinny(int dtype, bool gated, const FfnGemm &a, int cols, hipStream_t s);
+hipError_t launch_ffn_skinny(int dtype, bool gated, const FfnGemm &a, int rows, int cols,
+                             hipStream_t s);
 hipError_t launch_ffn_finish(int dtype, bool gated, const FfnGemm &a, hipStream_t s);
 
 // dZ = dY act'(Z) (dz null: not written; act none: dZ = dY) and the column sums

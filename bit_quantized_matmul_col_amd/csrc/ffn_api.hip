@@ -83,7 +83,8 @@ BackLayout back_layout(int64_t M, int64_t K, int64_t N, int grads) {
   o += up((size_t)M * K * 2);
   L.bias = o;
   if (grads == 1) o += up((size_t)bias_rows(M, N) * N * 4);
-  const FfnPlan tx{false, L.plan.tile, L.plan.xsplit}, tw{false, L.plan.tile, L.plan.wsplit};
+  const FfnPlan tx{false, L.plan.tile, L.plan.xsplit, 0},
+      tw{false, L.plan.tile, L.plan.wsplit, 0};
   auto room = [](size_t x, size_t y) { return up(x > y ? x : y); };
   L.part_x = o;
   o += room(ffn_part_bytes(L.plan.x, M, K, 1), ffn_part_bytes(tx, M, K, 1));

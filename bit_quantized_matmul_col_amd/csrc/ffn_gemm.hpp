@@ -67,15 +67,20 @@ __device__ inline int part_begin(int n, int split, int parts) {
   return (int)((uint64_t)n * split / (uint32_t)parts);
 }
 
-// Tile and part of block bid. The blocks of one XCD (they are dealt out round
-// robin) take consecutive places in the order parts, groups of up to 8 tile rows,
+// The blocks of one XCD (they are dealt out round robin) take consecutive places.
+__device__ inline uint32_t xcd_place(uint32_t bid, uint32_t blocks) {
+  constexpr uint32_t X = gemm_detail::kXcds;
+  const uint32_t x = bid % X, rem = blocks % X;
+  return x * (blocks / X) + (x < rem ? x : rem) + bid / X;
+}
+
+// Tile and part of block bid. The places of xcd_place are in the order parts, groups of up to 8 tile rows,
 // columns, rows of the group, so that an XCD works on few parts and neighbouring
 // tiles and its L2 serves the operands that they share.
 __device__ inline void tile_at(uint32_t bid, uint32_t tiles_m, uint32_t tiles_n, uint32_t parts,
                                int &tm, int &tn, int &part) {
-  constexpr uint32_t X = gemm_detail::kXcds, GM = gemm_detail::kGroupM;
-  const uint32_t tiles = tiles_m * tiles_n, nb = tiles * parts, x = bid % X, rem = nb % X;
-  const uint32_t place = x * (nb / X) + (x < rem ? x : rem) + bid / X;
+  constexpr uint32_t GM = gemm_detail::kGroupM;
+  const uint32_t tiles = tiles_m * tiles_n, place = xcd_place(bid, tiles * parts);
   part = (int)(place / tiles);
   const uint32_t v = place % tiles;
   const uint32_t first = v / (GM * tiles_n) * GM, in = v % (GM * tiles_n);
@@ -171,9 +176,12 @@ struct ColKTile {
   int cols;  // columns of the matrix from the tile's first on
 
   // Half a wave reads 8 rows (r % 16 in 0 .. 3 and 8 .. 11, or 4 more) x 2 chunks;
-  // rows of 8 chunks lie in opposite halves of the banks by twos already.
+  // rows of 8 chunks lie in opposite halves of the banks by twos already, rows of 4
+  // in four quarters.
   __device__ static int key(int r) {
-    return CH >= 16 ? 2 * ((r & 3) | (r >> 1 & 4)) : 2 * ((r >> 1 & 1) | (r >> 2 & 2));
+    return CH >= 16  ? 2 * ((r & 3) | (r >> 1 & 4))
+           : CH == 8 ? 2 * ((r >> 1 & 1) | (r >> 2 & 2))
+                     : 2 * (r >> 3 & 1);
   }
 
   __device__ void init(int64_t ld, int64_t ncols, int64_t) {
@@ -192,10 +200,10 @@ struct ColKTile {
     rsrc_t rs;
   };
   __device__ Stage stage(const uint8_t *mat, int64_t ld, int k, int len) const {
+    // len >= k: 0 rows at least (and n at most 0 then, as cols <= ld), so that nothing wraps
     const int left = len - k, rows = left < kStep ? left : kStep;
-    // (with `left` below 1 the product could wrap)
-    const int n = left > 0 ? ((rows - 1) * (int)ld + cols) * 2 : 0;
-    return Stage{make_rsrc(mat + 2 * (int64_t)k * ld, n)};
+    const int n = ((rows - 1) * (int)ld + cols) * 2;
+    return Stage{make_rsrc(mat + 2 * (int64_t)k * ld, n > 0 ? n : 0)};
   }
   __device__ void load(const Stage &st, uint8_t *to, int j) const {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rs, (lptr_t)(to + (wave_id() + NW * j) * 1024), 16,
@@ -374,7 +382,9 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, int col
   };
   auto loads_of = [&](int s) {
     const int seg = s >= n1 && a.segs > 1;
-    const int k = (s - (seg ? n1 : 0)) * kStep, len = s < s1 ? (int)a.K : 0;
+    // (clamping len - k instead makes the compiler build the resources in vector
+    // registers, with a loop around every load: 6 % slower)
+    const int k = (s - (seg ? n1 : 0)) * kStep, len = s < s1 ? (int)a.K : k;
     const uint8_t *b0 = seg ? pb[1] : pb[0];
     return Loads{A.stage(seg ? pa[1] : pa[0], a.lda, k, len), B.stage(b0, a.ldb, k, len),
                  C::GATED ? B.stage(pb[1], a.ldb, k, len) : B.stage(b0, a.ldb, k, len)};

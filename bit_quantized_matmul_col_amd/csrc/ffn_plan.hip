@@ -30,7 +30,7 @@ namespace llmint8 {
 namespace {
 
 constexpr int64_t kCus = kFfnCus;
-constexpr int64_t kFewMaxM = 384;
+constexpr int64_t kFewMaxM = 512;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -56,12 +56,6 @@ int64_t tile_blocks(const Shape &s, int tile, int parts) {
 double larger(double a, double b) {
   const double hi = a > b ? a : b, r = (a > b ? b : a) / hi, r2 = r * r;
   return hi * (1.0 + 0.1225 * r2 * r2 * r2);
-}
-
-// Two times that overlap only in part: within 2 % of (a^q + b^q)^(1/q), q = 0.786.
-double joined(double a, double b) {
-  const double hi = a > b ? a : b, r = (a > b ? b : a) / hi;
-  return hi * (1.0 + 0.369 * std::sqrt(r) + 1.046 * r);
 }
 
 // Microseconds of a launch of square tiles: rounds of as many blocks as the chip
@@ -101,20 +95,27 @@ double tile_us(const Shape &s, int tile, int parts) {
   return larger(t, floor);
 }
 
-// Microseconds of the few-row kernel: what one CU takes for its blocks' bytes and
-// what the whole chip takes for the weights (and for reading them again for
-// further groups of rows).
-double few_us(const Shape &s, int cols, int parts) {
-  const int mt = s.M <= 16 ? 1 : s.M <= 32 ? 2 : 4, p = s.gated() ? 2 : 1;
-  const int64_t groups = cdiv(s.M, 16 * mt), tiles = cdiv(s.N, cols);
-  const double st = (double)cdiv(cdiv(s.red, 128), parts);
-  const double kb = st * 4 * (p * cols * 64 + mt * 1024) * 1e-3;  // per block
+int64_t few_blocks(const Shape &s, int cols, int rows, int parts) {
+  return cdiv(s.N, cols) * cdiv(s.M, rows) * parts;
+}
+
+// Microseconds of the few-row kernel: what a CU takes for its blocks' bytes (it has
+// about 256 lines of 128 bytes on their way at a time, so that blocks of 32 columns
+// take as long for a row as those of 64), what the chip takes for the weights (and
+// for reading them again, from the caches, for further groups of rows), and the join.
+double few_us(const Shape &s, int cols, int rows, int parts) {
+  const int c = cols == 32 ? 0 : cols == 64 ? 1 : 2, p = s.gated() ? 2 : 1, mt = rows / 16;
+  const double cu_rate[3] = {63.4, 85.9, 96.7}, chip_rate[3] = {5.21, 6.47, 7.39};
+  const int64_t groups = cdiv(s.M, rows), tiles = cdiv(s.N, cols);
+  const int step = cols == 32 ? 64 : 32;
+  const double st = (double)cdiv(cdiv(cdiv(s.red, step), parts), 4);  // stages of a wave
+  const double kb = st * 4e-3 * step * (p * cols * 2 + 0.706 * mt * 32);  // per block
   const double wmb = 2e-6 * (double)s.red * (double)s.N * p;
-  const double xmb = 2e-6 * (double)(tiles * groups * s.red) * 16 * mt + (double)(groups - 1) * wmb;
-  const double cu = kb / (cols == 64 ? 91.0 : 94.7) * (double)cdiv(tiles * groups * parts, kCus);
-  const double chip = wmb / (cols == 64 ? 8.42 : 10.0) + xmb / 63.1;
-  double t = 2.26 + 0.253 * mt * p * cols / 64 + joined(cu, chip);
-  if (parts > 1) t += 2.4 + 0.394 * s.part_mb(parts);
+  const double xmb = 2e-6 * (double)(tiles * groups * s.red) * rows + (double)(groups - 1) * wmb;
+  const double rounds = (double)cdiv(few_blocks(s, cols, rows, parts), kCus);
+  double t = 2.3 + rounds * (0.31 + 0.33 * mt * p * cols / 64 + kb / cu_rate[c]) +
+             wmb / chip_rate[c] + xmb / 300.0;
+  if (parts > 1) t += 2.5 + 0.435 * s.part_mb(parts);
   return t;
 }
 
@@ -122,30 +123,31 @@ double few_us(const Shape &s, int cols, int parts) {
 
 FfnPlan ffn_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int outs) {
   const Shape s{kind, M, N, K * segs, outs};
-  FfnPlan best{false, 256, 1};
+  FfnPlan best{false, 256, 1, 0};
   double best_us = 1e300;
-  auto consider = [&](bool few, int tile, int parts, double us) {
+  auto consider = [&](bool few, int tile, int parts, int rows, double us) {
     // A host takes about 15 us for a call of two launches with a workspace and 10
     // for one launch, and gains nothing from a split that the GPU ends before (16.5:
     // the estimates of whole few-row launches are up to a quarter high there).
     if (parts > 1) us = us + 1.0 < 16.5 ? 16.5 : us + 1.0;
-    if (us < best_us) best = FfnPlan{few, tile, parts}, best_us = us;
+    if (us < best_us) best = FfnPlan{few, tile, parts, rows}, best_us = us;
   };
   const int64_t stages = cdiv(s.red, 64);
   for (const int parts : {1, 2, 3, 4, 6, 8}) {
     if (parts > 1 && stages < 3 * parts) break;
     // more parts than fill the chip once only add partial sums
     if (parts == 1 || tile_blocks(s, 256, parts) <= kCus)
-      consider(false, 256, parts, tile_us(s, 256, parts));
+      consider(false, 256, parts, 0, tile_us(s, 256, parts));
     if (parts == 1 || tile_blocks(s, 128, parts) <= 2 * kCus)
-      consider(false, 128, parts, tile_us(s, 128, parts));
+      consider(false, 128, parts, 0, tile_us(s, 128, parts));
     if ((s.gated() || kind == FfnKind::Forward) && M <= kFewMaxM)
-      for (const int cols : {64, 128}) {
-        // 128-column blocks: one group of rows, whose joined sums fit in LDS
-        if (cols == 128 && M > (s.gated() ? 32 : 64)) continue;
-        if (parts == 1 || cdiv(N, cols) * cdiv(M, 64) * parts <= kCus)
-          consider(true, cols, parts, few_us(s, cols, parts));
-      }
+      for (const int rows : {16, 32, 64})
+        for (const int cols : {32, 64, 128}) {
+          if (rows > 16 && rows / 2 >= M) continue;
+          if (rows == 64 && (cols == 32 || (cols == 128 && s.gated()))) continue;
+          if (parts == 1 || few_blocks(s, cols, rows, parts) <= kCus)
+            consider(true, cols, parts, rows, few_us(s, cols, rows, parts));
+        }
   }
   return best;
 }
@@ -222,7 +224,7 @@ hipError_t launch_ffn(FfnKind kind, int dtype, const FfnGemm &args, const FfnPla
   a.ksplit = p.ksplit;
   hipError_t e = hipSuccess;
   if (p.few)
-    e = launch_ffn_skinny(dtype, kind == FfnKind::Gated, a, p.tile, s);
+    e = launch_ffn_skinny(dtype, kind == FfnKind::Gated, a, p.rows, p.tile, s);
   else if (kind == FfnKind::Forward)
     e = launch_ffn_forward(dtype, a, p.tile, s);
   else if (kind == FfnKind::Gated)

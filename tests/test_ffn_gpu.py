@@ -76,7 +76,12 @@ SHAPES = [(1, 8, 8), (1, 1040, 520), (2, 4096, 1032), (7, 72, 24), (16, 256, 128
           # 256-tiles; 256-tiles with and without a tail of half tiles
           (5, 11008, 520), (3, 520, 28680), (1, 11008, 4096), (20, 4096, 11008), (40, 4104, 1032),
           (500, 2056, 1032), (1025, 8200, 2056), (2100, 2056, 4104), (1400, 4104, 4104),
-          (2300, 1032, 8200)]
+          (2300, 1032, 8200),
+          # few rows in groups of 16, 32 and 64 with blocks of 32, 64 and 128 columns, split
+          # and whole
+          (18, 4408, 5192), (70, 9304, 1880), (69, 264, 14080), (1, 4664, 4976), (465, 80, 520),
+          (372, 10200, 168), (17, 7840, 2544), (42, 9496, 1640), (1, 10776, 1552),
+          (55, 7264, 656), (167, 6880, 472), (310, 72, 776)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
