@@ -6,7 +6,8 @@
 // by many short blocks rather than by loops. Measured (MI355X):
 //   pack, unpack        4096 x 13824 bf16     29, 27 us (5.9, 6.4 TB/s)
 //   gated gradients     2048 x 11008 fp16     38 us (225 MB, 5.9 TB/s)
-//   activation's        2048 x 4096 bf16, with the bias gradient 18 us (50 MB)
+//   activation's        2048 x 4096 bf16, with the bias gradient 14.8 us (50 MB),
+//                       4096 x 11008 50 us (5.4 TB/s)
 //   join                2 parts of 2048 x 4096, residual 16 us (101 MB, 6.3 TB/s)
 #include "ffn_gemm.hpp"
 
@@ -110,8 +111,9 @@ __global__ __launch_bounds__(kThreads) void k_gated_grad(int act, const uint16_t
 // dz = dy act'(z) and, with part, the column sums of dz over this block's rows:
 // each thread sums its own rows, LDS joins the block's, k_bias_join the blocks'.
 // Always in the same order, so the result does not vary. A thread's rows go four
-// at a time, with their loads in flight together (2048 x 4096 bf16 with the bias
-// gradient: 20 us one row at a time).
+// at a time, with their loads in flight together, so a grid of one row a thread, which
+// suits the passes above, would waste the other three (4096 x 64 x 11008 without the
+// bias gradient: 167 us for the whole call against 100).
 template <class T>
 __global__ __launch_bounds__(kThreads) void k_act_grad(int act, const uint16_t *dy, int64_t lddy,
                                                        const uint16_t *z, int64_t ldz, int64_t M,
@@ -163,32 +165,39 @@ __global__ __launch_bounds__(kThreads) void k_act_grad(int act, const uint16_t *
   }
 }
 
-// dbias[n] = sum of the row blocks' partial sums; a block takes 64 columns, its
-// 16 waves every sixteenth row block, 8 loads at a time.
-constexpr int kJoinWaves = 16;
-__global__ __launch_bounds__(64 * kJoinWaves) void k_bias_join(const float *part, int64_t rows,
-                                                               int64_t N, float *dbias) {
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t n = (int64_t)blockIdx.x * 64 + lane;
-  float sum = 0.f;
-  if (n < N)
-    for (int64_t r0 = wv; r0 < rows; r0 += 8 * kJoinWaves) {
-      float v[8];
+// dbias[n] = sum of the row blocks' partial sums, in a fixed order. A block takes 64
+// columns: each thread 4 of them in every 64th row block, 4 loads in flight, joined in
+// LDS in two steps.
+constexpr int kJoinThreads = 1024;
+__global__ __launch_bounds__(kJoinThreads) void k_bias_join(const float *part, int64_t rows,
+                                                            int64_t N, float *dbias) {
+  const int t = threadIdx.x, q4 = t % 16 * 4, r = t / 16;
+  const int64_t n0 = (int64_t)blockIdx.x * 64;
+  f32x4 sum = {};
+  if (n0 + q4 < N)  // N is a multiple of 8
+    for (int64_t r0 = r; r0 < rows; r0 += 4 * 64) {
+      f32x4 v[4];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int64_t r = r0 + q * kJoinWaves;
-        v[q] = r < rows ? part[r * N + n] : 0.f;
+      for (int q = 0; q < 4; ++q) {
+        const int64_t i = r0 + q * 64;
+        v[q] = i < rows ? *(const f32x4 *)(part + i * N + n0 + q4) : f32x4{};
       }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) sum += v[q];
-    }
-  __shared__ float s[kJoinWaves][64];
-  s[wv][lane] = sum;
-  __syncthreads();
-  if (wv == 0 && n < N) {
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
-    for (int w = 1; w < kJoinWaves; ++w) sum += s[w][lane];
-    dbias[n] = sum;
+        for (int e = 0; e < 4; ++e) sum[e] += v[q][e];
+    }
+  __shared__ float s[64][64], s2[16][64];
+  *(f32x4 *)&s[r][q4] = sum;
+  __syncthreads();
+  const int c = t % 64, g = t / 64;
+  s2[g][c] = s[4 * g][c] + s[4 * g + 1][c] + s[4 * g + 2][c] + s[4 * g + 3][c];
+  __syncthreads();
+  if (t < 64 && n0 + t < N) {
+    float d = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) d += s2[w][t];
+    dbias[n0 + t] = d;
   }
 }
 
@@ -261,30 +270,29 @@ hipError_t launch_gated_grad(int dtype, int act, const uint16_t *dh, int64_t ldd
   return hipGetLastError();
 }
 
-// Row blocks of the bias gradient: enough blocks for the chip (1024 in all), at
-// least 16 rows a thread where there are as many.
+// Row blocks of the activation's gradient: a thread's rows in fours (see k_act_grad),
+// as few as leave no more than 256 row blocks for k_bias_join, or 512 blocks in all
+// where the columns are few. 2048 x 4096 with the bias gradient, 8 rows a thread 14.8 us,
+// 4 (512 row blocks) 16.6, 16 18.2; 4096 x 11008 16 rows 50.0, 48 69.0.
 int64_t bias_rows(int64_t M, int64_t N) {
   const RowGrid g = row_grid(M, N, kMaxGridY);
-  const int64_t ry = kThreads >> g.cx_log2;
-  int64_t rows = (M + 16 * ry - 1) / (16 * ry);
-  const int64_t want = (1024 + g.grid.x - 1) / g.grid.x;
-  if (rows > want) rows = want;
-  return rows;
+  const int64_t ry = kThreads >> g.cx_log2, all = 512 / (int64_t)g.grid.x;
+  const int64_t most = all > 256 ? all : 256;
+  const int64_t per = 4 * ((M + 4 * ry * most - 1) / (4 * ry * most));  // rows a thread
+  return (M + ry * per - 1) / (ry * per);
 }
 
 hipError_t launch_act_grad(int dtype, int act, const uint16_t *dy, int64_t lddy, const uint16_t *z,
                            int64_t ldz, int64_t M, int64_t N, uint16_t *dz, int64_t lddz,
                            float *dbias, float *part, hipStream_t s) {
-  const int64_t rows = dbias ? bias_rows(M, N) : kMaxGridY;
-  const RowGrid g = row_grid(M, N, rows);
+  const RowGrid g = row_grid(M, N, bias_rows(M, N));
   auto *kern = dtype == LLMINT8_FP16 ? k_act_grad<Half> : k_act_grad<Bfloat>;
   hipLaunchKernelGGL(kern, g.grid, dim3(kThreads), 0, s, act, dy, lddy, z, ldz, M, N, dz, lddz,
                      dbias ? part : nullptr, g.cx_log2);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && dbias) {
-    hipLaunchKernelGGL(k_bias_join, dim3((unsigned)((N + 63) / 64)), dim3(64 * kJoinWaves), 0, s,
-                       part,
-                       (int64_t)g.grid.y, N, dbias);
+    hipLaunchKernelGGL(k_bias_join, dim3((unsigned)((N + 63) / 64)), dim3(kJoinThreads), 0, s,
+                       part, (int64_t)g.grid.y, N, dbias);
     e = hipGetLastError();
   }
   return e;
