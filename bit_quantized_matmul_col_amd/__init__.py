@@ -541,19 +541,33 @@ def _activation(name: str) -> int:
 
 def _matrix(t, name: str, like: torch.Tensor, shape=None) -> int:
     """The leading dimension of a matrix of like's dtype and device."""
-    # the checks in the order of what a valid call needs; the named errors below
-    if (isinstance(t, torch.Tensor) and t.dtype is like.dtype and t.is_cuda and t.dim() == 2
-            and t.device == like.device):
-        M, N = got = tuple(t.shape)
-        s0, s1 = t.stride()
-        if M and N and (s1 == 1 or N == 1) and (shape is None or got == shape):
-            return s0 if M > 1 else N
+    # what a valid matrix passes, by the cheapest queries (a call is a few microseconds);
+    # the named errors below
+    if isinstance(t, torch.Tensor) and t.dtype is like.dtype and t.dim() == 2:
+        device, got = t.get_device(), t.shape
+        if device >= 0 and device == like.get_device() and (shape is None or got == shape):
+            M, N = got
+            if M and N:
+                if t.is_contiguous():
+                    return N
+                s0, s1 = t.stride()
+                if s1 == 1:
+                    return s0 if M > 1 else N
     _need(t, name, like.dtype, 2)
     if shape is not None:
         _need_shape(t, name, shape)
     if t.device != like.device:
         raise ValueError(f"{name} must be on {like.device}, got {t.device}")
     return _ld(t, name)
+
+
+def _vector(t, name: str, dtype, n: int, like: torch.Tensor) -> int:
+    """The address of a contiguous vector of n elements on like's device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n
+            and t.is_contiguous() and t.get_device() == like.get_device()):
+        _need_vec(t, name, dtype, n)
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    return t.data_ptr()
 
 
 def _out(t, name: str, like: torch.Tensor, shape):
@@ -661,6 +675,9 @@ def llmint8_checkpoint_unpack(checkpoint: Checkpoint, dtype=torch.float16, *,
     return X
 
 
+_MATMUL_OPTS_SIZE = C.sizeof(MatmulOpts)
+
+
 def llmint8_matmul_workspace_size(M: int, K: int, N: int) -> int:
     return int(lib().llmint8_matmul_workspace_size(M, K, N))
 
@@ -684,17 +701,15 @@ def llmint8_matmul(X: torch.Tensor, W: torch.Tensor, *, bias: torch.Tensor | Non
     Y, ldy = _out(Y, "Y", X, (M, N))
     opts = None
     if act or bias is not None or residual is not None or Z is not None:
-        o = MatmulOpts(C.sizeof(MatmulOpts), act)
+        b = r = z = None
+        ldr = ldz = 0
         if bias is not None:
-            _need_vec(bias, "bias", X.dtype, N)
-            o.bias = bias.data_ptr()
+            b = _vector(bias, "bias", X.dtype, N, X)
         if residual is not None:
-            o.ldr = _matrix(residual, "residual", X, (M, N))
-            o.residual = residual.data_ptr()
+            ldr, r = _matrix(residual, "residual", X, (M, N)), residual.data_ptr()
         if Z is not None:
-            o.ldz = _matrix(Z, "Z", X, (M, N))
-            o.Z = Z.data_ptr()
-        opts = C.byref(o)
+            ldz, z = _matrix(Z, "Z", X, (M, N)), Z.data_ptr()
+        opts = C.byref(MatmulOpts(_MATMUL_OPTS_SIZE, act, b, r, ldr, z, ldz))
     L = lib()
     ws, nb, keep = _workspace(workspace, L.llmint8_matmul_workspace_size(M, K, N), X)
     _check(L.llmint8_matmul(X.data_ptr(), M, K, ldx, W.data_ptr(), ldw, N, dt, Y.data_ptr(), ldy,
@@ -740,7 +755,7 @@ def llmint8_matmul_backward(dY: torch.Tensor, X, W: torch.Tensor | None, *,
     if act != LLMINT8_ACT_NONE:
         if Z is None:
             raise ValueError("Z is needed with an activation")
-        z, ldz = Z.data_ptr(), _matrix(Z, "Z", dY, (M, N))
+        ldz, z = _matrix(Z, "Z", dY, (M, N)), Z.data_ptr()
     dX, lddx = _out(dX, "dX", dY, (M, K)) if need_dX else (None, 0)
     dW, lddw = _out(dW, "dW", dY, (K, N)) if need_dW else (None, 0)
     if not need_dbias:
@@ -748,7 +763,7 @@ def llmint8_matmul_backward(dY: torch.Tensor, X, W: torch.Tensor | None, *,
     elif dbias is None:
         dbias = torch.empty((N,), dtype=torch.float32, device=dY.device)
     else:
-        _need_vec(dbias, "dbias", torch.float32, N)
+        _vector(dbias, "dbias", torch.float32, N, dY)
     L = lib()
     ws, nb, keep = _workspace(workspace, L.llmint8_matmul_backward_workspace_size(M, K, N), dY)
     _check(L.llmint8_matmul_backward(dY.data_ptr(), M, N, lddy, x, K, _ptr(W), ldw, z, ldz, act, dt,

@@ -121,7 +121,9 @@ double few_us(const Shape &s, int cols, int rows, int parts) {
 
 }  // namespace
 
-FfnPlan ffn_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int outs) {
+namespace {
+
+FfnPlan best_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int outs) {
   const Shape s{kind, M, N, K * segs, outs};
   FfnPlan best{false, 256, 1, 0};
   double best_us = 1e300;
@@ -150,6 +152,23 @@ FfnPlan ffn_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int ou
         }
   }
   return best;
+}
+
+}  // namespace
+
+// A call and its workspace query ask for the same plan one after the other, which
+// takes up to 0.6 us to find: each thread keeps the last one with its shape.
+FfnPlan ffn_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int outs) {
+  thread_local struct {
+    FfnKind kind;
+    int64_t M, N, K;
+    int segs, outs;
+    FfnPlan plan;
+  } last{};  // M = 0: none yet
+  if (M != last.M || N != last.N || K != last.K || kind != last.kind || segs != last.segs ||
+      outs != last.outs)
+    last = {kind, M, N, K, segs, outs, best_plan(kind, M, N, K, segs, outs)};
+  return last.plan;
 }
 
 namespace {
@@ -185,8 +204,8 @@ double together_us(const Shape &x, int xparts, const Shape &w, int wparts, int t
 // gated 2048 x 4096 x 11008 694 -> 671, gated 4096 x 5120 x 13824 2165 -> 1890. The
 // tile and the parts chosen by the estimates cost 1.5 % more than the best ones.
 FfnBackPlan ffn_back_plan(int64_t M, int64_t K, int64_t N, int grads) {
-  FfnBackPlan p{ffn_plan(FfnKind::GradX, M, K, N, grads, 1),
-                ffn_plan(FfnKind::GradW, K, N, M, 1, grads), 256, 1, 1};
+  FfnBackPlan p{best_plan(FfnKind::GradX, M, K, N, grads, 1),
+                best_plan(FfnKind::GradW, K, N, M, 1, grads), 256, 1, 1};
   const Shape x{FfnKind::GradX, M, K, N * grads, 1}, w{FfnKind::GradW, K, N, M, grads};
   double best = 1e300;
   const int64_t stx = cdiv(x.red, 64), stw = cdiv(w.red, 64);
