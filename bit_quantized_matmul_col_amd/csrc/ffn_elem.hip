@@ -4,7 +4,8 @@
 // bound by HBM; a thread owns 8 consecutive columns (16 bytes) of a row, and the
 // grid holds a block per 256 chunks, so that the chip's memory system is kept full
 // by many short blocks rather than by loops. Measured (MI355X):
-//   pack, unpack        4096 x 13824 bf16     29, 27 us (5.9, 6.4 TB/s)
+//   pack, unpack        4096 x 13824 bf16     36, 31 us (4.7, 5.5 TB/s; with 2 or 4
+//                       rows a thread in flight 35 to 36 and 32 to 33)
 //   gated gradients     2048 x 11008 fp16     38 us (225 MB, 5.9 TB/s)
 //   activation's        2048 x 4096 bf16, with the bias gradient 14.8 us (50 MB),
 //                       4096 x 11008 50 us (5.4 TB/s)

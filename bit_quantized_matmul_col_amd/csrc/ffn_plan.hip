@@ -1,20 +1,23 @@
 // Which kernel a 16-bit product takes.
 //
 // The candidates are square tiles of 256 or 128 rows and columns and, for the
-// forward products of up to kFewMaxM rows, the few-row kernel with 64- or
-// 128-column blocks, each with the reduction whole or split into up to 8 parts.
-// The plan is the candidate with the smallest estimated time. The estimates are
-// sums of a few terms whose constants were fitted to 3850 timed launches on
-// MI355X (bf16; M 1 to 4096, K and N 256 to 28672, every candidate, all four
-// products): they are within 7 % (256-tiles), 8 % (128-tiles) and 11 % (few rows)
-// of the measured times (root mean square), and the plans chosen by them cost
-// 0.7 % more than the best candidate (geometric mean over the shapes, 33 % at
-// worst). Some of the choices, in microseconds:
-//   1 x 4096 x 4096       few rows, 64 columns: whole 12.5, 4 parts 11.4 (one by one from
-//                         a host 12.0 against 14.9)
-//   1 x 8192 x 28672      few rows: 128 columns 87.7, 64 columns 105.4
-//   300 x 1040 x 520      few rows 8.0, 128-tiles in 4 parts 11.2
-//   256 x 4096 x 4096     few rows 21.9, 128-tiles in 4 parts 23.3, whole 37.7
+// forward products of up to kFewMaxM rows, the few-row kernel with blocks of 32, 64
+// or 128 columns and 16, 32 or 64 rows, each with the reduction whole or split into
+// up to 8 parts. The plan is the candidate with the smallest estimated time. The
+// estimates are sums of a few terms whose constants were fitted to 3900 timed
+// launches of square tiles (M 1 to 4096, all four products) and 6500 of the few-row
+// kernel (M 1 to 512) on MI355X (bf16; K and N 256 to 28672, every candidate): they
+// are within 7 % (256-tiles), 8 % (128-tiles) and 6 % (few rows) of the measured
+// times (root mean square). The plans chosen by them cost 1 % more than the best
+// candidate (geometric mean over the shapes; at worst 33 % with the square tiles,
+// 19 % over 289 forward shapes of up to 512 rows). Some of the choices, in microseconds:
+//   1 x 4096 x 4096       few rows: 32 columns 12.5, 64 13.0, in 4 parts 11.8 (one by one
+//                         from a host 12.0 against 14.8)
+//   1 x 8192 x 28672      few rows: 128 columns 89.9, 64 columns 106.4
+//   64 x 2048 x 2048      few rows: 32 columns by 16 rows 7.4, 64 by 64 11.8
+//   300 x 1040 x 520      few rows 5.9, 128-tiles in 4 parts 11.2
+//   256 x 4096 x 4096     few rows, 64 by 64 21.7, 32 by 16 53.9; 128-tiles in 4 parts
+//                         23.3, whole 37.7
 //   2048 x 4096 x 4096    dX: 128-tiles 62.6, 256-tiles in 2 parts 75.5
 //   2048 x 11008 x 4096   256-tiles in 2 parts 158, whole 212; 128-tiles 164
 //   2048 x 4096 x 11008   gated: 256-tiles 293, 128-tiles 410
@@ -128,10 +131,9 @@ FfnPlan best_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int o
   FfnPlan best{false, 256, 1, 0};
   double best_us = 1e300;
   auto consider = [&](bool few, int tile, int parts, int rows, double us) {
-    // A host takes about 15 us for a call of two launches with a workspace and 10
-    // for one launch, and gains nothing from a split that the GPU ends before (16.5:
-    // the estimates of whole few-row launches are up to a quarter high there).
-    if (parts > 1) us = us + 1.0 < 16.5 ? 16.5 : us + 1.0;
+    // A host takes 12 to 15 us for a call of two launches with a workspace, 8 to 10 for
+    // one launch, and gains nothing from a split that the GPU ends before.
+    if (parts > 1) us = us + 1.0 < 15.0 ? 15.0 : us + 1.0;
     if (us < best_us) best = FfnPlan{few, tile, parts, rows}, best_us = us;
   };
   const int64_t stages = cdiv(s.red, 64);
