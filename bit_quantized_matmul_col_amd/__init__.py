@@ -577,6 +577,10 @@ def _out(t, name: str, like: torch.Tensor, shape):
     return t, _matrix(t, name, like, shape)
 
 
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
 def _raw_stream(t: torch.Tensor) -> int:
     """torch's current stream of t's device, as the hipStream_t itself."""
     return torch._C._cuda_getCurrentRawStream(t.device.index)
@@ -600,18 +604,17 @@ def _c_checkpoint(c: Checkpoint) -> SavedMatrix:
 def _checkpoint(c, name: str, device, shape=None) -> SavedMatrix:
     """The C view of a checkpoint, after checking it."""
     codes, scales = c
-    # as in _matrix, what a valid one needs first
+    # as in _matrix, what a valid one passes first
     if (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor)
-            and codes.dtype is torch.int8 and scales.dtype is torch.uint8
-            and codes.device == device and scales.device == device and codes.is_cuda
-            and codes.dim() == 2):
-        M, K = got = tuple(codes.shape)
-        (s0, s1), blocks = codes.stride(), -(-K // CHECKPOINT_BLOCK)
-        if (M > 1 and K and s1 == 1 and s0 >= (K + 15) // 16 * 16
-                and (shape is None or got == shape) and tuple(scales.shape) == (M, blocks)):
-            t0, t1 = scales.stride()
-            if t1 == 1 or blocks == 1:
-                return SavedMatrix(codes.data_ptr(), s0, scales.data_ptr(), t0)
+            and codes.dtype is torch.int8 and scales.dtype is torch.uint8 and codes.dim() == 2):
+        index, got = codes.get_device(), codes.shape
+        if (index >= 0 and index == device.index and scales.get_device() == index
+                and (shape is None or got == shape)):
+            M, K = got
+            (s0, s1), blocks = codes.stride(), -(-K // CHECKPOINT_BLOCK)
+            if (M > 1 and K and s1 == 1 and s0 >= (K + 15) // 16 * 16
+                    and scales.shape == (M, blocks) and scales.is_contiguous()):
+                return SavedMatrix(codes.data_ptr(), s0, scales.data_ptr(), blocks)
     _need(codes, f"{name}.codes", torch.int8, 2)
     if shape is not None:
         _need_shape(codes, f"{name}.codes", shape)
@@ -766,9 +769,9 @@ def llmint8_matmul_backward(dY: torch.Tensor, X, W: torch.Tensor | None, *,
         _vector(dbias, "dbias", torch.float32, N, dY)
     L = lib()
     ws, nb, keep = _workspace(workspace, L.llmint8_matmul_backward_workspace_size(M, K, N), dY)
-    _check(L.llmint8_matmul_backward(dY.data_ptr(), M, N, lddy, x, K, _ptr(W), ldw, z, ldz, act, dt,
-                                     _ptr(dX), lddx, _ptr(dW), lddw, _ptr(dbias), ws, nb,
-                                     _raw_stream(dY)))
+    _check(L.llmint8_matmul_backward(dY.data_ptr(), M, N, lddy, x, K, _address(W), ldw, z, ldz,
+                                     act, dt, _address(dX), lddx, _address(dW), lddw,
+                                     _address(dbias), ws, nb, _raw_stream(dY)))
     return dX, dW, dbias
 
 
@@ -853,6 +856,6 @@ def llmint8_gated_backward(dH: torch.Tensor, X, Wg: torch.Tensor, Wu: torch.Tens
     L = lib()
     ws, nb, keep = _workspace(workspace, L.llmint8_gated_backward_workspace_size(M, K, N), dH)
     _check(L.llmint8_gated_backward(dH.data_ptr(), M, N, lddh, x, K, Wg.data_ptr(), Wu.data_ptr(),
-                                    ldw, C.byref(g), C.byref(u), act, dt, _ptr(dX), lddx,
-                                    _ptr(dWg), _ptr(dWu), lddw, ws, nb, _raw_stream(dH)))
+                                    ldw, C.byref(g), C.byref(u), act, dt, _address(dX), lddx,
+                                    _address(dWg), _address(dWu), lddw, ws, nb, _raw_stream(dH)))
     return dX, dWg, dWu
