@@ -71,9 +71,18 @@ struct FfnBackPlan {
 };
 // dZ is [M x N], X [M x K]; grads: gradients of one (1) or two (2) products.
 FfnBackPlan ffn_back_plan(int64_t M, int64_t K, int64_t N, int grads);
-hipError_t launch_ffn_together(int dtype, const FfnGemm &x, const FfnGemm &w, const FfnBackPlan &p,
-                               hipStream_t s);
-hipError_t launch_ffn_back(int dtype, const FfnGemm &x, const FfnGemm &w, int tile, hipStream_t s);
+// The bias gradient's last step, dbias[n] = the sum of `rows` partial sums part[r][n]
+// (dbias null: none).
+struct BiasJoin {
+  const float *part;
+  int64_t rows, N;
+  float *dbias;
+};
+hipError_t launch_ffn_together(int dtype, const FfnGemm &x, const FfnGemm &w, const BiasJoin &j,
+                               const FfnBackPlan &p, hipStream_t s);
+hipError_t launch_ffn_back(int dtype, const FfnGemm &x, const FfnGemm &w, const BiasJoin &j,
+                           int tile, hipStream_t s);
+hipError_t launch_bias_join(const BiasJoin &j, hipStream_t s);
 
 // The plan's kernel and, for a split reduction, the pass that joins the parts.
 // dtype: 0 fp16, 1 bf16.
@@ -87,12 +96,12 @@ hipError_t launch_ffn_skinny(int dtype, bool gated, const FfnGemm &a, int rows, 
                              hipStream_t s);
 hipError_t launch_ffn_finish(int dtype, bool gated, const FfnGemm &a, hipStream_t s);
 
-// dZ = dY act'(Z) (dz null: not written; act none: dZ = dY) and the column sums
-// of dZ: dbias [N] fp32 through part, bias_rows(M, N) x N floats.
+// dZ = dY act'(Z) (dz null: not written; act none: dZ = dY) and, with part, partial
+// column sums of dZ: bias_rows(M, N) x N floats, for a BiasJoin.
 int64_t bias_rows(int64_t M, int64_t N);
 hipError_t launch_act_grad(int dtype, int act, const uint16_t *dy, int64_t lddy, const uint16_t *z,
                            int64_t ldz, int64_t M, int64_t N, uint16_t *dz, int64_t lddz,
-                           float *dbias, float *part, hipStream_t s);
+                           float *part, hipStream_t s);
 
 // A saved matrix: 16 bits (scales null) or 8-bit codes.
 struct Saved {

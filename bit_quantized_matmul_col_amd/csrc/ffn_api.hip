@@ -112,6 +112,7 @@ struct Grads {
   int64_t lddx;
   uint16_t *dW[2];
   int64_t lddw;
+  BiasJoin bias;
 };
 
 hipError_t run_grads(int dtype, const Grads &g, int64_t M, int64_t K, int64_t N, uint8_t *ws,
@@ -140,8 +141,10 @@ hipError_t run_grads(int dtype, const Grads &g, int64_t M, int64_t K, int64_t N,
     w.ldy = g.lddw;
     w.part = (float *)(ws + L.part_w);
   }
-  if (g.dX && g.dW[0]) return launch_ffn_together(dtype, x, w, L.plan, s);
-  hipError_t e = g.dX ? launch_ffn(FfnKind::GradX, dtype, x, L.plan.x, s) : hipSuccess;
+  if (g.dX && g.dW[0]) return launch_ffn_together(dtype, x, w, g.bias, L.plan, s);
+  hipError_t e = g.bias.dbias ? launch_bias_join(g.bias, s) : hipSuccess;
+  if (e != hipSuccess) return e;
+  e = g.dX ? launch_ffn(FfnKind::GradX, dtype, x, L.plan.x, s) : hipSuccess;
   if (e == hipSuccess && g.dW[0]) e = launch_ffn(FfnKind::GradW, dtype, w, L.plan.w, s);
   return e;
 }
@@ -238,15 +241,17 @@ LLMINT8_EXPORT int llmint8_matmul_backward(const uint16_t *dY, int64_t M, int64_
   uint8_t *ws = (uint8_t *)workspace;
   const bool act = activation != LLMINT8_ACT_NONE, products = dX || dW;
   uint16_t *own = (uint16_t *)(ws + L.dz);
+  float *part = (float *)(ws + L.bias);
   const uint16_t *dz = act ? own : dY;
   const int64_t lddz = act ? pitch8(N) : lddy;
   hipError_t e = hipSuccess;
   if (act || dbias)
     e = launch_act_grad(dtype, activation, dY, lddy, Z, ldz, M, N, act && products ? own : nullptr,
-                        lddz, dbias, (float *)(ws + L.bias), s);
-  if (e == hipSuccess && products)
+                        lddz, dbias ? part : nullptr, s);
+  if (e == hipSuccess)
     e = run_grads(dtype, Grads{1, {dz, nullptr}, lddz, X, {W, nullptr}, ldw, dX, lddx,
-                               {dW, nullptr}, lddw}, M, K, N, ws, L, s);
+                               {dW, nullptr}, lddw, {part, bias_rows(M, N), N, dbias}},
+                  M, K, N, ws, L, s);
   return hip_status(e);
 }
 
@@ -324,7 +329,7 @@ LLMINT8_EXPORT int llmint8_gated_backward(const uint16_t *dH, int64_t M, int64_t
   hipError_t e = launch_gated_grad(dtype, activation, dH, lddh, saved_of(G), saved_of(U), M, N, dg,
                                    du, lddz, s);
   if (e == hipSuccess)
-    e = run_grads(dtype, Grads{2, {dg, du}, lddz, X, {Wg, Wu}, ldw, dX, lddx, {dWg, dWu}, lddw}, M,
-                  K, N, ws, L, s);
+    e = run_grads(dtype, Grads{2, {dg, du}, lddz, X, {Wg, Wu}, ldw, dX, lddx, {dWg, dWu}, lddw, {}},
+                  M, K, N, ws, L, s);
   return hip_status(e);
 }

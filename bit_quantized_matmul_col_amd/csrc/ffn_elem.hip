@@ -110,7 +110,7 @@ __global__ __launch_bounds__(kThreads) void k_gated_grad(int act, const uint16_t
 }
 
 // dz = dy act'(z) and, with part, the column sums of dz over this block's rows:
-// each thread sums its own rows, LDS joins the block's, k_bias_join the blocks'.
+// each thread sums its own rows, LDS joins the block's, join_bias the blocks'.
 // Always in the same order, so the result does not vary. A thread's rows go four
 // at a time, with their loads in flight together, so a grid of one row a thread, which
 // suits the passes above, would waste the other three (4096 x 64 x 11008 without the
@@ -166,40 +166,10 @@ __global__ __launch_bounds__(kThreads) void k_act_grad(int act, const uint16_t *
   }
 }
 
-// dbias[n] = sum of the row blocks' partial sums, in a fixed order. A block takes 64
-// columns: each thread 4 of them in every 64th row block, 4 loads in flight, joined in
-// LDS in two steps.
 constexpr int kJoinThreads = 1024;
-__global__ __launch_bounds__(kJoinThreads) void k_bias_join(const float *part, int64_t rows,
-                                                            int64_t N, float *dbias) {
-  const int t = threadIdx.x, q4 = t % 16 * 4, r = t / 16;
-  const int64_t n0 = (int64_t)blockIdx.x * 64;
-  f32x4 sum = {};
-  if (n0 + q4 < N)  // N is a multiple of 8
-    for (int64_t r0 = r; r0 < rows; r0 += 4 * 64) {
-      f32x4 v[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t i = r0 + q * 64;
-        v[q] = i < rows ? *(const f32x4 *)(part + i * N + n0 + q4) : f32x4{};
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum[e] += v[q][e];
-    }
-  __shared__ float s[64][64], s2[16][64];
-  *(f32x4 *)&s[r][q4] = sum;
-  __syncthreads();
-  const int c = t % 64, g = t / 64;
-  s2[g][c] = s[4 * g][c] + s[4 * g + 1][c] + s[4 * g + 2][c] + s[4 * g + 3][c];
-  __syncthreads();
-  if (t < 64 && n0 + t < N) {
-    float d = 0.f;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) d += s2[w][t];
-    dbias[n0 + t] = d;
-  }
+__global__ __launch_bounds__(kJoinThreads) void k_bias_join(BiasJoin j) {
+  __shared__ float s[64 * 64];
+  ffn::join_bias<kJoinThreads>(j, blockIdx.x, s);
 }
 
 // Sums of the parts s0, s0 + 1, ... of 8 columns, in the order of the parts; the
@@ -272,7 +242,7 @@ hipError_t launch_gated_grad(int dtype, int act, const uint16_t *dh, int64_t ldd
 }
 
 // Row blocks of the activation's gradient: a thread's rows in fours (see k_act_grad),
-// as few as leave no more than 256 row blocks for k_bias_join, or 512 blocks in all
+// as few as leave no more than 256 row blocks for join_bias, or 512 blocks in all
 // where the columns are few. 2048 x 4096 with the bias gradient, 8 rows a thread 14.8 us,
 // 4 (512 row blocks) 16.6, 16 18.2; 4096 x 11008 16 rows 50.0, 48 69.0.
 int64_t bias_rows(int64_t M, int64_t N) {
@@ -285,18 +255,17 @@ int64_t bias_rows(int64_t M, int64_t N) {
 
 hipError_t launch_act_grad(int dtype, int act, const uint16_t *dy, int64_t lddy, const uint16_t *z,
                            int64_t ldz, int64_t M, int64_t N, uint16_t *dz, int64_t lddz,
-                           float *dbias, float *part, hipStream_t s) {
+                           float *part, hipStream_t s) {
   const RowGrid g = row_grid(M, N, bias_rows(M, N));
   auto *kern = dtype == LLMINT8_FP16 ? k_act_grad<Half> : k_act_grad<Bfloat>;
   hipLaunchKernelGGL(kern, g.grid, dim3(kThreads), 0, s, act, dy, lddy, z, ldz, M, N, dz, lddz,
-                     dbias ? part : nullptr, g.cx_log2);
-  hipError_t e = hipGetLastError();
-  if (e == hipSuccess && dbias) {
-    hipLaunchKernelGGL(k_bias_join, dim3((unsigned)((N + 63) / 64)), dim3(kJoinThreads), 0, s,
-                       part, (int64_t)g.grid.y, N, dbias);
-    e = hipGetLastError();
-  }
-  return e;
+                     part, g.cx_log2);
+  return hipGetLastError();
+}
+
+hipError_t launch_bias_join(const BiasJoin &j, hipStream_t s) {
+  hipLaunchKernelGGL(k_bias_join, dim3((unsigned)((j.N + 63) / 64)), dim3(kJoinThreads), 0, s, j);
+  return hipGetLastError();
 }
 
 hipError_t launch_ffn_finish(int dtype, bool gated, const FfnGemm &a, hipStream_t s) {

@@ -295,6 +295,45 @@ __device__ inline void load_f8(const float *p, float *v) {
   for (int e = 0; e < 4; ++e) v[e] = x[e], v[4 + e] = y[e];
 }
 
+// Columns 64 block .. + 63 of a BiasJoin, the same sums in the same order for every
+// number of THREADS: 64 streams take every 64th partial sum, a thread 4 columns of
+// 1024 / THREADS streams with 4 loads of each in flight; they meet in s, 64 x 64 floats.
+template <int THREADS>
+__device__ inline void join_bias(const BiasJoin &j, int64_t block, float *s) {
+  constexpr int V = 1024 / THREADS, STEP = THREADS / 16;
+  const int t = threadIdx.x, q4 = t % 16 * 4, r = t / 16;
+  const int64_t n0 = block * 64;
+  f32x4 sum[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) sum[k] = f32x4{};
+  if (n0 + q4 < j.N)  // N is a multiple of 8
+    for (int64_t r0 = r; r0 < j.rows; r0 += 4 * 64) {
+      f32x4 v[V][4];
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t i = r0 + k * STEP + q * 64;
+          v[k][q] = i < j.rows ? *(const f32x4 *)(j.part + i * j.N + n0 + q4) : f32x4{};
+        }
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[k][e] += v[k][q][e];
+    }
+#pragma unroll
+  for (int k = 0; k < V; ++k) *(f32x4 *)(s + (r + k * STEP) * 64 + q4) = sum[k];
+  __syncthreads();
+  if (t < 64 && n0 + t < j.N) {
+    float d = 0.f;
+#pragma unroll 16
+    for (int i = 0; i < 64; ++i) d += s[i * 64 + t];
+    j.dbias[n0 + t] = d;
+  }
+}
+
 // ---- kernel ---------------------------------------------------------------------------
 
 template <Lay L, int N, int NW>

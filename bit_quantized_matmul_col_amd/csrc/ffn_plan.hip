@@ -229,11 +229,11 @@ size_t ffn_part_bytes(const FfnPlan &p, int64_t M, int64_t N, int outs) {
   return p.ksplit > 1 ? (size_t)p.ksplit * outs * M * N * 4 : 0;
 }
 
-hipError_t launch_ffn_together(int dtype, const FfnGemm &x, const FfnGemm &w, const FfnBackPlan &p,
-                               hipStream_t s) {
+hipError_t launch_ffn_together(int dtype, const FfnGemm &x, const FfnGemm &w, const BiasJoin &j,
+                               const FfnBackPlan &p, hipStream_t s) {
   FfnGemm gx = x, gw = w;
   gx.ksplit = p.xsplit, gw.ksplit = p.wsplit;
-  hipError_t e = launch_ffn_back(dtype, gx, gw, p.tile, s);
+  hipError_t e = launch_ffn_back(dtype, gx, gw, j, p.tile, s);
   if (e == hipSuccess && p.xsplit > 1) e = launch_ffn_finish(dtype, false, gx, s);
   if (e == hipSuccess && p.wsplit > 1) e = launch_ffn_finish(dtype, false, gw, s);
   return e;
