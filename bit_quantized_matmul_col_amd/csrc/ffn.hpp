@@ -57,6 +57,10 @@ inline int64_t tail_cut(int64_t rows, int64_t cols, int64_t parts) {
   return 2 * rows * (cols - cut) <= kFfnCus ? cut : cols;
 }
 
+// A launch of at most one 128-tile per CU runs with a ring of four stages, which covers the
+// latency that the second block of a CU covers otherwise (see launch_order).
+inline bool deep_ring(int64_t blocks128) { return blocks128 <= kFfnCus; }
+
 enum class FfnKind { Forward, Gated, GradX, GradW };
 
 FfnPlan ffn_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int outs);

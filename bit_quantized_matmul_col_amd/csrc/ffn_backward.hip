@@ -56,8 +56,9 @@ hipError_t launch_back_tile(const FfnGemm &x, const FfnGemm &w, const BiasJoin &
                             hipStream_t s) {
   if (tile == 256) return launch_back<T, 256, 256, 2, 4, 2>(x, w, j, s);
   using C = Cfg<T, Lay::RowK, Lay::RowK, false, 128, 128, 2, 2>;
-  return blocks_of<C>(x) + blocks_of<C>(w) <= kFfnCus ? launch_back<T, 128, 128, 2, 2, 4>(x, w, j, s)
-                                                      : launch_back<T, 128, 128, 2, 2, 2>(x, w, j, s);
+  return deep_ring((int64_t)blocks_of<C>(x) + blocks_of<C>(w))
+             ? launch_back<T, 128, 128, 2, 2, 4>(x, w, j, s)
+             : launch_back<T, 128, 128, 2, 2, 2>(x, w, j, s);
 }
 
 }  // namespace ffn

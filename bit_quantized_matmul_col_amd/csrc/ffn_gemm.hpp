@@ -618,7 +618,7 @@ hipError_t launch_order(const FfnGemm &a, int tile, hipStream_t stream) {
   if (tile == 256) return launch_tiles<Wide, Tail>(a, stream);
   const int64_t blocks = (a.M + 127) / 128 * ((a.N + Small::OUTN - 1) / Small::OUTN) * a.outs *
                          a.ksplit;
-  return blocks <= kFfnCus ? launch_tiles<Deep, Deep>(a, stream)
+  return deep_ring(blocks) ? launch_tiles<Deep, Deep>(a, stream)
                            : launch_tiles<Small, Small>(a, stream);
 }
 
