@@ -662,7 +662,8 @@ def llmint8_checkpoint_pack(X: torch.Tensor) -> Checkpoint:
 
 def llmint8_checkpoint_unpack(checkpoint: Checkpoint, dtype=torch.float16, *,
                               X=None) -> torch.Tensor:
-    """What a checkpoint stands for, as a 16-bit matrix [M, K] of `dtype`."""
+    """What a checkpoint stands for, as a 16-bit matrix [M, K] of `dtype`. Exact in bf16, and
+    in fp16 if it was packed from fp16; rounded (to infinity from 65520 on) otherwise."""
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
     codes = checkpoint[0]

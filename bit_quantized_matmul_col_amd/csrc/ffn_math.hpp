@@ -129,8 +129,10 @@ __device__ inline void with_act(int act, F f) {
 // ---- 8-bit checkpoint blocks ---------------------------------------------------------
 // 32 entries of a row share the scale 2^e, e = floor(log2 max|x|) - 6 (at least
 // -127), held as the byte e + 127; code = clamp(rint(x 2^-e), -127, 127) and the
-// entry stands for code 2^e: seven significant bits, exact in fp16 and bf16, so
-// a product takes it without a second rounding. A block with an infinity or a
+// entry stands for code 2^e: seven significant bits, exact in bf16, and in fp16 where
+// the entries were fp16 themselves, so a product takes a checkpointed X without a second
+// rounding. (Sums below 2^-18 or above 65504, as G and U may hold in an fp16 block, are
+// not exact in fp16; their gradients read them in fp32.) A block with an infinity or a
 // NaN takes the byte 255 and zero codes and stands for NaN throughout.
 
 __device__ inline float ckpt_scale(uint32_t byte) {

@@ -315,7 +315,10 @@ int llmint8_linear_fp8(const uint16_t *X, int64_t M, int64_t K, int64_t ldx,
  * Checkpoint format: 32 consecutive entries of a row (the last block of a row
  * may be shorter) share the scale 2^e, e = max(floor(log2 max|x|) - 6, -127),
  * held as the byte e + 127; code = clamp(rint(x 2^-e), -127, 127), ties to
- * even, and the entry stands for code 2^e. That value is exact in fp16 and bf16.
+ * even, and the entry stands for code 2^e. That value is exact in bf16, and in
+ * fp16 where the matrix was packed from fp16; otherwise (bf16 entries, G and U from
+ * their fp32 sums) expanding it to fp16 rounds steps below 2^-24 and gives infinity
+ * from 65520 on.
  * A block that holds an infinity or a NaN takes the byte 255 and stands for NaN.
  *   data     codes [M x ld], ld a multiple of 16.
  *   scales   [M x ld_scales] bytes, ld_scales >= ceil(columns / 32).
@@ -366,7 +369,7 @@ int llmint8_matmul(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, const u
  * (dbias fp32, from the unrounded dZ). The residual's gradient is dY itself.
  * Each output may be NULL: not computed. X may be NULL without dW, W without dX,
  * Z when activation is LLMINT8_ACT_NONE (it is not read then).
- *   X  16 bits or an 8-bit checkpoint.
+ *   X  16 bits or an 8-bit checkpoint (expanded to `dtype` first).
  *   workspace  llmint8_matmul_backward_workspace_size(M, K, N) bytes.
  */
 size_t llmint8_matmul_backward_workspace_size(int64_t M, int64_t K, int64_t N);
@@ -394,7 +397,8 @@ int llmint8_gated(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, const ui
  * (rounded to 16 bits, the products' operands),
  *   dX = dG . Wg^T + dU . Wu^T,  dWg = X^T . dG,  dWu = X^T . dU.
  * dX may be NULL (Wg and Wu are not read then); dWg and dWu both or neither
- * (X is not read then). G and U as the forward pass saved them, X likewise.
+ * (X is not read then). G and U as the forward pass saved them, X likewise;
+ * checkpointed G and U are read in fp32, a checkpointed X is expanded to `dtype`.
  *   workspace  llmint8_gated_backward_workspace_size(M, K, N) bytes.
  */
 size_t llmint8_gated_backward_workspace_size(int64_t M, int64_t K, int64_t N);
