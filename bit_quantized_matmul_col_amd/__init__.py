@@ -150,8 +150,17 @@ def _check(status: int):
         raise Llmint8Error(status, llmint8_status_string(status))
 
 
-def _stream(t: torch.Tensor):
-    return C.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+def _launch(call, t: torch.Tensor, *args, opts=()):
+    """call(*args, stream, *opts) with torch's current stream of t's device, and that device
+    the current one: a default stream's handle names no device, and the launches behind it
+    go to the current one, where t's addresses mean nothing."""
+    index = t.get_device()
+    if index == torch._C._cuda_getDevice():
+        status = call(*args, torch._C._cuda_getCurrentRawStream(index), *opts)
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, torch._C._cuda_getCurrentRawStream(index), *opts)
+    _check(status)
 
 
 def _ptr(t):
@@ -211,8 +220,7 @@ def llmint8_quantize_colwise(W: torch.Tensor):
     K, N = W.shape
     Wq = torch.empty((N, K), dtype=torch.int8, device=W.device)
     s = torch.empty((N,), dtype=torch.float32, device=W.device)
-    _check(lib().llmint8_quantize_colwise(_ptr(W), K, N, _ld(W, "W"), _ptr(Wq), _ptr(s),
-                                          _stream(W)))
+    _launch(lib().llmint8_quantize_colwise, W, _ptr(W), K, N, _ld(W, "W"), _ptr(Wq), _ptr(s))
     return Wq, s
 
 
@@ -229,9 +237,8 @@ def llmint8_find_outliers(X: torch.Tensor, threshold: float = 6.0, workspace=Non
     need = llmint8_find_outliers_workspace_size(M, K)
     if workspace is None:
         workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=X.device)
-    _check(lib().llmint8_find_outliers(_ptr(X), M, K, _ld(X, "X"), float(threshold), _ptr(idx),
-                                       _ptr(count), *_ws(workspace),
-                                       _stream(X)))
+    _launch(lib().llmint8_find_outliers, X, _ptr(X), M, K, _ld(X, "X"), float(threshold), _ptr(idx),
+            _ptr(count), *_ws(workspace))
     return idx, count
 
 
@@ -247,8 +254,8 @@ def llmint8_quantize_rowwise(X: torch.Tensor, idx: torch.Tensor | None = None,
         _need_vec(count, "count", torch.int32, 1, exact=False)
     Xq = torch.empty((M, K), dtype=torch.int8, device=X.device)
     m = torch.empty((M,), dtype=torch.float32, device=X.device)
-    _check(lib().llmint8_quantize_rowwise(_ptr(X), M, K, _ld(X, "X"), _ptr(idx), _ptr(count),
-                                          _ptr(Xq), _ptr(m), _stream(X)))
+    _launch(lib().llmint8_quantize_rowwise, X, _ptr(X), M, K, _ld(X, "X"), _ptr(idx), _ptr(count),
+            _ptr(Xq), _ptr(m))
     return Xq, m
 
 
@@ -318,11 +325,11 @@ def llmint8_linear(X: torch.Tensor, Wq: torch.Tensor, col_absmax: torch.Tensor,
         opts = o
     args = (_ptr(X), M, K, _ld(X, "X"), _ptr(Wq), _ptr(col_absmax), _ptr(W),
             _ld(W, "W") if W is not None else N, N, float(threshold), _ptr(Y), _ld(Y, "Y"),
-            _ptr(outlier_count), _ptr(C_debug), *_ws(workspace), _stream(X))
+            _ptr(outlier_count), _ptr(C_debug), *_ws(workspace))
     if opts is None:
-        _check(lib().llmint8_linear(*args))
+        _launch(lib().llmint8_linear, X, *args)
     else:
-        _check(lib().llmint8_linear_ex(*args, C.byref(opts)))
+        _launch(lib().llmint8_linear_ex, X, *args, opts=(C.byref(opts),))
     return Y
 
 
@@ -357,10 +364,9 @@ def llmint8_linear_noalloc(X: torch.Tensor, Wq: torch.Tensor, col_absmax: torch.
     if C_debug is not None:
         _need(C_debug, "C_debug", torch.int32)
         _need_shape(C_debug, "C_debug", (M, N), contiguous=True)
-    _check(lib().llmint8_linear_noalloc(
-        _ptr(X), M, K, _ld(X, "X"), _ptr(Wq), _ptr(col_absmax), _ptr(W),
-        _ld(W, "W") if W is not None else N, N, float(threshold), _ptr(Y), _ld(Y, "Y"),
-        _ptr(outlier_count), _ptr(C_debug), _stream(X)))
+    _launch(lib().llmint8_linear_noalloc, X, _ptr(X), M, K, _ld(X, "X"), _ptr(Wq), _ptr(col_absmax),
+            _ptr(W), _ld(W, "W") if W is not None else N, N, float(threshold), _ptr(Y), _ld(Y, "Y"),
+            _ptr(outlier_count), _ptr(C_debug))
     return Y
 
 
@@ -377,8 +383,8 @@ def llmint8_quantize_tensorwise(W: torch.Tensor, workspace=None):
     if workspace is None:
         workspace = torch.empty((max(llmint8_quantize_tensorwise_workspace_size(K, N), 1),),
                                 dtype=torch.uint8, device=W.device)
-    _check(lib().llmint8_quantize_tensorwise(_ptr(W), K, N, _ld(W, "W"), _ptr(Wq), _ptr(sw),
-                                             *_ws(workspace), _stream(W)))
+    _launch(lib().llmint8_quantize_tensorwise, W, _ptr(W), K, N, _ld(W, "W"), _ptr(Wq), _ptr(sw),
+            *_ws(workspace))
     return Wq, sw
 
 
@@ -413,10 +419,9 @@ def llmint8_linear_tensorwise(X: torch.Tensor, Wq: torch.Tensor, w_absmax: torch
     if workspace is None:
         workspace = torch.empty((llmint8_linear_tensorwise_workspace_size(M, K, N),),
                                 dtype=torch.uint8, device=X.device)
-    _check(lib().llmint8_linear_tensorwise(
-        _ptr(X), M, K, _ld(X, "X"), _ptr(Wq), _ptr(w_absmax), N, _ptr(bias), _ptr(Y),
-        _ld(Y, "Y"), _ptr(x_absmax), _ptr(C_debug), *_ws(workspace),
-        _stream(X)))
+    _launch(lib().llmint8_linear_tensorwise, X, _ptr(X), M, K, _ld(X, "X"), _ptr(Wq),
+            _ptr(w_absmax), N, _ptr(bias), _ptr(Y), _ld(Y, "Y"), _ptr(x_absmax), _ptr(C_debug),
+            *_ws(workspace))
     return Y
 
 
@@ -428,8 +433,7 @@ def llmint8_quantize_colwise_fp8(W: torch.Tensor):
     K, N = W.shape
     Wq = torch.empty((N, K), dtype=torch.uint8, device=W.device)
     s = torch.empty((N,), dtype=torch.float32, device=W.device)
-    _check(lib().llmint8_quantize_colwise_fp8(_ptr(W), K, N, _ld(W, "W"), _ptr(Wq), _ptr(s),
-                                              _stream(W)))
+    _launch(lib().llmint8_quantize_colwise_fp8, W, _ptr(W), K, N, _ld(W, "W"), _ptr(Wq), _ptr(s))
     return Wq, s
 
 
@@ -445,8 +449,8 @@ def llmint8_quantize_rowwise_fp8(X: torch.Tensor, idx: torch.Tensor | None = Non
         _need_vec(count, "count", torch.int32, 1, exact=False)
     Xq = torch.empty((M, K), dtype=torch.uint8, device=X.device)
     m = torch.empty((M,), dtype=torch.float32, device=X.device)
-    _check(lib().llmint8_quantize_rowwise_fp8(_ptr(X), M, K, _ld(X, "X"), _ptr(idx), _ptr(count),
-                                              _ptr(Xq), _ptr(m), _stream(X)))
+    _launch(lib().llmint8_quantize_rowwise_fp8, X, _ptr(X), M, K, _ld(X, "X"), _ptr(idx),
+            _ptr(count), _ptr(Xq), _ptr(m))
     return Xq, m
 
 
@@ -502,11 +506,9 @@ def llmint8_linear_fp8(X: torch.Tensor, Wq8: torch.Tensor, col_absmax: torch.Ten
                    bias=bias.data_ptr() if bias is not None else None,
                    y_col_absmax=y_col_absmax.data_ptr() if y_col_absmax is not None else None,
                    x_col_absmax=x_col_absmax.data_ptr() if x_col_absmax is not None else None)
-    _check(lib().llmint8_linear_fp8(
-        _ptr(X), M, K, _ld(X, "X"), _ptr(Wq8), _ptr(col_absmax), _ptr(W),
-        _ld(W, "W") if W is not None else N, N, float(threshold), _ptr(Y), _ld(Y, "Y"),
-        _ptr(outlier_count), _ptr(C_debug), *_ws(workspace), _stream(X),
-        C.byref(o)))
+    _launch(lib().llmint8_linear_fp8, X, _ptr(X), M, K, _ld(X, "X"), _ptr(Wq8), _ptr(col_absmax),
+            _ptr(W), _ld(W, "W") if W is not None else N, N, float(threshold), _ptr(Y), _ld(Y, "Y"),
+            _ptr(outlier_count), _ptr(C_debug), *_ws(workspace), opts=(C.byref(o),))
     return Y
 
 
@@ -581,11 +583,6 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(t: torch.Tensor) -> int:
-    """torch's current stream of t's device, as the hipStream_t itself."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
-
-
 def _new_checkpoint(M: int, K: int, device) -> Checkpoint:
     codes = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=device)
     if K % 16:
@@ -646,7 +643,10 @@ def _workspace(workspace, need: int, like: torch.Tensor):
             return None, 0, None
         workspace = torch.empty((need,), dtype=torch.uint8, device=like.device)
         return workspace.data_ptr(), need, workspace
-    return *_ws(workspace), workspace
+    ws = *_ws(workspace), workspace
+    if workspace.get_device() != like.get_device():
+        raise ValueError(f"workspace must be on {like.device}, got {workspace.device}")
+    return ws
 
 
 def llmint8_checkpoint_pack(X: torch.Tensor) -> Checkpoint:
@@ -655,8 +655,8 @@ def llmint8_checkpoint_pack(X: torch.Tensor) -> Checkpoint:
     ldx = _matrix(X, "X", X)
     M, K = X.shape
     c = _new_checkpoint(M, K, X.device)
-    _check(lib().llmint8_checkpoint_pack(X.data_ptr(), M, K, ldx, dt, C.byref(_c_checkpoint(c)),
-                                         _raw_stream(X)))
+    _launch(lib().llmint8_checkpoint_pack, X, X.data_ptr(), M, K, ldx, dt,
+            C.byref(_c_checkpoint(c)))
     return c
 
 
@@ -674,8 +674,8 @@ def llmint8_checkpoint_unpack(checkpoint: Checkpoint, dtype=torch.float16, *,
         X, ldx = torch.empty((M, K), dtype=dtype, device=codes.device), K
     else:
         ldx = _matrix(X, "X", torch.empty((0,), dtype=dtype, device=codes.device), (M, K))
-    _check(lib().llmint8_checkpoint_unpack(C.byref(saved), M, K, _DTYPES[dtype], X.data_ptr(), ldx,
-                                           _raw_stream(X)))
+    _launch(lib().llmint8_checkpoint_unpack, X, C.byref(saved), M, K, _DTYPES[dtype], X.data_ptr(),
+            ldx)
     return X
 
 
@@ -716,8 +716,8 @@ def llmint8_matmul(X: torch.Tensor, W: torch.Tensor, *, bias: torch.Tensor | Non
         opts = C.byref(MatmulOpts(_MATMUL_OPTS_SIZE, act, b, r, ldr, z, ldz))
     L = lib()
     ws, nb, keep = _workspace(workspace, L.llmint8_matmul_workspace_size(M, K, N), X)
-    _check(L.llmint8_matmul(X.data_ptr(), M, K, ldx, W.data_ptr(), ldw, N, dt, Y.data_ptr(), ldy,
-                            opts, ws, nb, _raw_stream(X)))
+    _launch(L.llmint8_matmul, X, X.data_ptr(), M, K, ldx, W.data_ptr(), ldw, N, dt, Y.data_ptr(),
+            ldy, opts, ws, nb)
     return Y
 
 
@@ -770,9 +770,8 @@ def llmint8_matmul_backward(dY: torch.Tensor, X, W: torch.Tensor | None, *,
         _vector(dbias, "dbias", torch.float32, N, dY)
     L = lib()
     ws, nb, keep = _workspace(workspace, L.llmint8_matmul_backward_workspace_size(M, K, N), dY)
-    _check(L.llmint8_matmul_backward(dY.data_ptr(), M, N, lddy, x, K, _address(W), ldw, z, ldz,
-                                     act, dt, _address(dX), lddx, _address(dW), lddw,
-                                     _address(dbias), ws, nb, _raw_stream(dY)))
+    _launch(L.llmint8_matmul_backward, dY, dY.data_ptr(), M, N, lddy, x, K, _address(W), ldw, z,
+            ldz, act, dt, _address(dX), lddx, _address(dW), lddw, _address(dbias), ws, nb)
     return dX, dW, dbias
 
 
@@ -814,8 +813,8 @@ def llmint8_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, *,
         g, u = C.byref(_c_checkpoint(G)), C.byref(_c_checkpoint(U))
     L = lib()
     ws, nb, keep = _workspace(workspace, L.llmint8_gated_workspace_size(M, K, N), X)
-    _check(L.llmint8_gated(X.data_ptr(), M, K, ldx, Wg.data_ptr(), Wu.data_ptr(), ldw, N, act, dt,
-                           H.data_ptr(), ldh, g, u, ws, nb, _raw_stream(X)))
+    _launch(L.llmint8_gated, X, X.data_ptr(), M, K, ldx, Wg.data_ptr(), Wu.data_ptr(), ldw, N, act,
+            dt, H.data_ptr(), ldh, g, u, ws, nb)
     return H if save == "none" else (H, G, U)
 
 
@@ -856,7 +855,7 @@ def llmint8_gated_backward(dH: torch.Tensor, X, Wg: torch.Tensor, Wu: torch.Tens
         dWg = dWu = None
     L = lib()
     ws, nb, keep = _workspace(workspace, L.llmint8_gated_backward_workspace_size(M, K, N), dH)
-    _check(L.llmint8_gated_backward(dH.data_ptr(), M, N, lddh, x, K, Wg.data_ptr(), Wu.data_ptr(),
-                                    ldw, C.byref(g), C.byref(u), act, dt, _address(dX), lddx,
-                                    _address(dWg), _address(dWu), lddw, ws, nb, _raw_stream(dH)))
+    _launch(L.llmint8_gated_backward, dH, dH.data_ptr(), M, N, lddh, x, K, Wg.data_ptr(),
+            Wu.data_ptr(), ldw, C.byref(g), C.byref(u), act, dt, _address(dX), lddx, _address(dWg),
+            _address(dWu), lddw, ws, nb)
     return dX, dWg, dWu

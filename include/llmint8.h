@@ -19,7 +19,8 @@
  * Conventions shared by every call:
  *   - Every pointer is a DEVICE pointer unless stated otherwise. fp16 data is
  *     passed as uint16_t IEEE binary16 bit patterns. `stream` is a hipStream_t
- *     (NULL = the default stream).
+ *     (NULL = the default stream). The device of the pointers and the stream has to
+ *     be the current one.
  *   - Matrices are row-major with an explicit leading dimension in elements.
  *   - The caller owns and allocates every buffer, including the workspace. The
  *     library never allocates device memory, keeps no state between calls and
