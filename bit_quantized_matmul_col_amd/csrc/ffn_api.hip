@@ -16,7 +16,6 @@ constexpr int64_t kMaxLd = (int64_t)1 << 21;  // 256 rows x 2 bytes x 2^21 = 2^3
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-int64_t pitch8(int64_t n) { return (n + 7) / 8 * 8; }
 int hip_status(hipError_t e) { return e == hipSuccess ? LLMINT8_OK : LLMINT8_ERR_HIP; }
 
 // The first failed check of a call; alignment faults rank below argument faults.
@@ -78,7 +77,7 @@ BackLayout back_layout(int64_t M, int64_t K, int64_t N, int grads) {
   L.plan = ffn_back_plan(M, K, N, grads);
   size_t o = 0;
   L.dz = o;
-  o += up((size_t)grads * M * pitch8(N) * 2);
+  o += up((size_t)grads * M * N * 2);
   L.x = o;
   o += up((size_t)M * K * 2);
   L.bias = o;
@@ -243,7 +242,7 @@ LLMINT8_EXPORT int llmint8_matmul_backward(const uint16_t *dY, int64_t M, int64_
   uint16_t *own = (uint16_t *)(ws + L.dz);
   float *part = (float *)(ws + L.bias);
   const uint16_t *dz = act ? own : dY;
-  const int64_t lddz = act ? pitch8(N) : lddy;
+  const int64_t lddz = act ? N : lddy;
   hipError_t e = hipSuccess;
   if (act || dbias)
     e = launch_act_grad(dtype, activation, dY, lddy, Z, ldz, M, N, act && products ? own : nullptr,
@@ -324,12 +323,11 @@ LLMINT8_EXPORT int llmint8_gated_backward(const uint16_t *dH, int64_t M, int64_t
   if (const int st = check_workspace(workspace, workspace_bytes, L.total)) return st;
   hipStream_t s = (hipStream_t)stream;
   uint8_t *ws = (uint8_t *)workspace;
-  const int64_t lddz = pitch8(N);
-  uint16_t *dg = (uint16_t *)(ws + L.dz), *du = dg + M * lddz;
+  uint16_t *dg = (uint16_t *)(ws + L.dz), *du = dg + M * N;
   hipError_t e = launch_gated_grad(dtype, activation, dH, lddh, saved_of(G), saved_of(U), M, N, dg,
-                                   du, lddz, s);
+                                   du, N, s);
   if (e == hipSuccess)
-    e = run_grads(dtype, Grads{2, {dg, du}, lddz, X, {Wg, Wu}, ldw, dX, lddx, {dWg, dWu}, lddw, {}},
+    e = run_grads(dtype, Grads{2, {dg, du}, N, X, {Wg, Wu}, ldw, dX, lddx, {dWg, dWu}, lddw, {}},
                   M, K, N, ws, L, s);
   return hip_status(e);
 }

@@ -105,14 +105,14 @@ template <int ROWS, int NW>
 struct RowKTile {
   static constexpr int PITCH = kStep * 2;    // bytes of a stored row
   static constexpr int BYTES = ROWS * PITCH;
-  static constexpr int CH = PITCH / 16;      // chunks per stored row
+  static constexpr int CH = PITCH / 16;      // chunks per stored row, 8
   static constexpr int RPI = 64 / CH;        // rows per 1 KB load
   static constexpr int G = ROWS / (RPI * NW);  // loads per wave per stage
   int bytes;  // of the tile's rows, from the first element to the last
   int voff[G];
   int chunk;      // first reduction step of this lane's chunk within a stage
 
-  __device__ static int key(int r) { return CH == 8 ? (r >> 1) & 7 : (r >> 2) & 3; }
+  __device__ static int key(int r) { return (r >> 1) & 7; }
 
   // rows: rows of the matrix from the tile's first on; len: the reduction length.
   __device__ void init(int64_t ld, int64_t rows, int64_t len) {
@@ -361,8 +361,6 @@ struct Cfg {
   static constexpr int SLABP = WN + 4;  // fp32 pitch of the epilogue's rows
   static constexpr int SLABS = NW * 32 * SLABP * 4;
   static constexpr int LDS = NST * STAGE > SLABS ? NST * STAGE : SLABS;
-  // waves per SIMD that the registers must leave room for
-  static constexpr int WPE = BM * BN / (NW * 64) > 128 ? 1 : 2;
   static constexpr int WO = GATED ? WN / 2 : WN;  // output columns of a wave
   static_assert(WO % 32 == 0, "a wave holds whole checkpoint blocks");
 };

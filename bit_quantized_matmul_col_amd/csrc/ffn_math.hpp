@@ -13,7 +13,6 @@ typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 struct Half {
-  typedef _Float16 elem;
   __device__ static float to_f(uint16_t u) { return (float)__builtin_bit_cast(_Float16, u); }
   __device__ static uint16_t from_f(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
   __device__ static f32x4 mfma16(s16x8 a, s16x8 b, f32x4 c) {
@@ -23,7 +22,6 @@ struct Half {
 };
 
 struct Bfloat {
-  typedef __bf16 elem;
   __device__ static float to_f(uint16_t u) { return __builtin_bit_cast(float, (uint32_t)u << 16); }
   __device__ static uint16_t from_f(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
   __device__ static f32x4 mfma16(s16x8 a, s16x8 b, f32x4 c) {
