@@ -513,6 +513,8 @@ def llmint8_linear_fp8(X: torch.Tensor, Wq8: torch.Tensor, col_absmax: torch.Ten
 
 
 # ---- 16-bit feed-forward operators ---------------------------------------------------
+# As the calls above, these record nothing for autograd: a result has no grad_fn, also where
+# an input requires grad. The backward functions are called explicitly.
 
 _DTYPES = {torch.float16: LLMINT8_FP16, torch.bfloat16: LLMINT8_BF16}
 _ACTIVATIONS = {"none": LLMINT8_ACT_NONE, "relu": LLMINT8_ACT_RELU, "gelu": LLMINT8_ACT_GELU,
@@ -693,7 +695,8 @@ def llmint8_matmul(X: torch.Tensor, W: torch.Tensor, *, bias: torch.Tensor | Non
     bias [N] and residual [M, N] of the same dtype -> Y [M, N].
 
     activation is "none", "relu", "gelu", "gelu_tanh" or "silu". Z, if given, receives the
-    pre-activations X W + bias [M, N] that llmint8_matmul_backward takes."""
+    pre-activations X W + bias [M, N] that llmint8_matmul_backward takes. Autograd does not
+    see the call: gradients come from llmint8_matmul_backward."""
     dt = _dtype_of(X, "X")
     ldx = _matrix(X, "X", X)
     M, K = X.shape
@@ -792,7 +795,8 @@ def llmint8_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, *,
     X [M, K], Wg and Wu [K, N] -> H [M, N].
 
     save "none" returns H; "full" returns (H, G, U) with the pre-activations G = X Wg and
-    U = X Wu in 16 bits, "8bit" returns them as Checkpoints."""
+    U = X Wu in 16 bits, "8bit" returns them as Checkpoints. Autograd does not see the call:
+    gradients come from llmint8_gated_backward."""
     dt = _dtype_of(X, "X")
     ldx = _matrix(X, "X", X)
     M, K = X.shape

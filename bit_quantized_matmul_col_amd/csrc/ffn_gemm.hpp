@@ -21,11 +21,14 @@
 //  * 16-byte chunks are permuted within each stored row (chunk c of row r sits at
 //    c ^ key(r)), so that the lanes of one LDS access fall in different bank
 //    groups: conflicts cost under 1 % of the LDS cycles.
-//  * Operands past the end of the matrix (rows, columns, reduction) read as
-//    zero: every load goes through a buffer resource that ends with the last
-//    element, and a RowK lane whose chunk lies past the reduction length takes
-//    an offset outside it. Both operands are zero there, so no infinity or NaN
-//    of a neighbouring row is multiplied by a zero.
+//  * Reduction steps past the end read as zero in both operands, so no infinity
+//    or NaN of a neighbouring row is multiplied by a zero: every load goes through
+//    a buffer resource that ends with the last element of the stage's last row,
+//    and a RowK lane whose chunk lies past the reduction length takes an offset
+//    outside it. Rows of a RowK tile past the matrix read as zero too. Columns of a
+//    ColK tile past the matrix read what lies behind them in memory (the gap
+//    between rows, the next row, zeros after the last): a column meets only its own
+//    outputs, and those past the matrix are not stored.
 //
 // A block computes BM x BN outputs with NWM x NWN waves. The MFMAs take the
 // operands in the order (B, A), so a lane's accumulators hold 4 consecutive
@@ -33,11 +36,12 @@
 // after which a lane owns 8 consecutive columns and every load and store of the
 // epilogue is 16 bytes.
 //
-// What bounds it: at 8192 x 8192 x 28672 (gated) the card's power. It runs at 1310
-// to 1345 TFLOP/s with the MFMA units busy 70 % of the time at 1.7 GHz; the library's
-// product of the same sizes reaches 1273. The LDS is active 28 % of the time. Smaller
-// products lose to partial rounds and to the epilogue, 7 to 9 us a round of 256-tiles
-// (33 MB written at once): 1177 TFLOP/s at 4096 x 5120 x 13824 with 8-bit G and U.
+// What bounds it: at 8192 x 8192 x 28672 (gated) the card's power. It runs at 1240
+// to 1345 TFLOP/s, by card and by what ran before, with the MFMA units busy 71 % of
+// the time at 1.65 to 1.73 GHz; the library's product of the same sizes reaches 1273.
+// The LDS is active 28 % of the time. Smaller products lose to partial rounds and to
+// the epilogue, 7 to 9 us a round of 256-tiles (33 MB written at once): 1020 to 1250
+// TFLOP/s at 4096 x 5120 x 13824 with 8-bit G and U.
 //
 // Measured against it at 8192 x 8192 x 28672: 32x32x16 MFMAs 6.12 against 5.72 ms (the
 // clock falls further for the same work), stages of 32 steps in rings of 4 or 5 10 %

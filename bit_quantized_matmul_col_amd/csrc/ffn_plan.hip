@@ -10,7 +10,11 @@
 // are within 7 % (256-tiles), 8 % (128-tiles) and 6 % (few rows) of the measured
 // times (root mean square). The plans chosen by them cost 1 % more than the best
 // candidate (geometric mean over the shapes; at worst 33 % with the square tiles,
-// 19 % over 289 forward shapes of up to 512 rows). Some of the choices, in microseconds:
+// 19 % over 289 forward shapes of up to 512 rows). The best candidate itself is far
+// from the bytes' and operations' floor between about 64 and 1000 rows (1.3 to 2.9
+// times it): groups of rows read W again from the caches, 128-tiles are too few for
+// the chip or, as tiles of dW over few rows, mostly fill and epilogue.
+// Some of the choices, in microseconds:
 //   1 x 4096 x 4096       few rows: 32 columns 12.5, 64 13.0, in 4 parts 11.8 (one by one
 //                         from a host 12.0 against 14.8)
 //   1 x 8192 x 28672      few rows: 128 columns 89.9, 64 columns 106.4
@@ -54,7 +58,7 @@ int64_t tile_blocks(const Shape &s, int tile, int parts) {
   return cdiv(s.M, tile) * cdiv(s.N, s.gated() ? tile / 2 : tile) * s.outs * parts;
 }
 
-// The larger of two times, a little more where they are close: within 0.5 % of
+// The larger of two times, a little more where they are close: within 0.9 % of
 // (a^6 + b^6)^(1/6), without the powers (a plan is made on every call).
 double larger(double a, double b) {
   const double hi = a > b ? a : b, r = (a > b ? b : a) / hi, r2 = r * r;
@@ -132,7 +136,8 @@ FfnPlan best_plan(FfnKind kind, int64_t M, int64_t N, int64_t K, int segs, int o
   double best_us = 1e300;
   auto consider = [&](bool few, int tile, int parts, int rows, double us) {
     // A host takes 12 to 15 us for a call of two launches with a workspace, 8 to 10 for
-    // one launch, and gains nothing from a split that the GPU ends before.
+    // one launch, and gains nothing from a split that the GPU ends before. (Under graph
+    // replay it would: 1 x 4096 x 4096 11.8 us in 4 parts against 12.5 whole.)
     if (parts > 1) us = us + 1.0 < 15.0 ? 15.0 : us + 1.0;
     if (us < best_us) best = FfnPlan{few, tile, parts, rows}, best_us = us;
   };
