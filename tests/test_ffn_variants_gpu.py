@@ -56,3 +56,13 @@ def test_matmul_backward(lm, M, K, N, dtype):
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_gated_backward(lm, M, K, N, dtype):
     base.test_gated_backward(lm, M, K, N, dtype, "full")
+
+
+def test_more_rows_than_the_grid_has(lm):
+    """70001 rows of one row a block: the row-streaming passes stride over a grid of 65535."""
+    M, K, N = 70001, 24, 2056
+    base.test_checkpoint(lm, M, N, BF16)
+    base.test_matmul(lm, M, K, N, BF16)
+    base.test_gated(lm, M, K, N, F16)
+    base.test_matmul_backward(lm, M, K, N, F16, "8bit")
+    base.test_gated_backward(lm, M, K, N, BF16, "8bit")
