@@ -33,6 +33,7 @@ LLMINT8_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 LLMINT8_FP16 = 0
 LLMINT8_BF16 = 1
+LLMINT8_FP32 = 2
 LLMINT8_ACT_NONE = 0
 LLMINT8_ACT_RELU = 1
 LLMINT8_ACT_GELU = 2
@@ -68,6 +69,19 @@ class MatmulOpts(C.Structure):
     _fields_ = [("struct_size", C.c_size_t), ("activation", C.c_int), ("bias", C.c_void_p),
                 ("residual", C.c_void_p), ("ldr", C.c_int64), ("Z", C.c_void_p),
                 ("ldz", C.c_int64)]
+
+
+class RouteOpts(C.Structure):
+    """Mirror of llmint8_route_opts."""
+    _fields_ = [("struct_size", C.c_size_t), ("scores", C.c_int), ("renormalize", C.c_int),
+                ("scale", C.c_float), ("groups", C.c_int), ("top_groups", C.c_int),
+                ("group_best", C.c_int), ("bias", C.c_void_p)]
+
+
+class ExpertRows(C.Structure):
+    """Mirror of llmint8_expert_rows."""
+    _fields_ = [("offsets", C.c_void_p), ("order", C.c_void_p), ("places", C.c_void_p),
+                ("E", C.c_int64), ("k", C.c_int64)]
 
 
 class Llmint8Error(RuntimeError):
@@ -126,6 +140,21 @@ def lib() -> C.CDLL:
         for name in ("matmul", "matmul_backward", "gated", "gated_backward"):
             query = getattr(L, f"llmint8_{name}_workspace_size")
             query.argtypes, query.restype = [i64, i64, i64], sz
+        L.llmint8_route.argtypes = [p, i64, i64, i64, i, i64, p, p, p, p]
+        L.llmint8_route_backward.argtypes = [p, p, i64, i64, i64, i, i64, p, p, p, i64, p]
+        L.llmint8_expert_plan.argtypes = [p, i64, i64, i64, p, p, p, p]
+        L.llmint8_experts_gated.argtypes = [p, i64, i64, i64, p, p, i64, i64, i64, p, p, i, i, p,
+                                            i64, p, p, i64, p, sz, p]
+        L.llmint8_experts_gated_backward.argtypes = [p, i64, i64, i64, p, i64, i64, p, p, i64, i64,
+                                                     p, p, i64, p, p, i, i, p, i64, p, p, i64,
+                                                     i64, p, p, sz, p]
+        L.llmint8_experts_matmul.argtypes = [p, i64, i64, i64, p, i64, i64, i64, p, p, i64, i, p,
+                                             i64, p, sz, p]
+        L.llmint8_experts_matmul_backward.argtypes = [p, i64, i64, i64, p, i64, i64, p, i64, i64,
+                                                      p, i, p, i64, p, i64, i64, p, sz, p]
+        for name in ("gated", "gated_backward", "matmul", "matmul_backward"):
+            query = getattr(L, f"llmint8_experts_{name}_workspace_size")
+            query.argtypes, query.restype = [i64] * 5, sz
         L.llmint8_status_string.argtypes = [C.c_int]
         L.llmint8_status_string.restype = C.c_char_p
         for name in ("llmint8_quantize_colwise", "llmint8_find_outliers",
@@ -135,7 +164,10 @@ def lib() -> C.CDLL:
                      "llmint8_quantize_colwise_fp8", "llmint8_quantize_rowwise_fp8",
                      "llmint8_linear_fp8", "llmint8_checkpoint_pack",
                      "llmint8_checkpoint_unpack", "llmint8_matmul", "llmint8_matmul_backward",
-                     "llmint8_gated", "llmint8_gated_backward"):
+                     "llmint8_gated", "llmint8_gated_backward", "llmint8_route",
+                     "llmint8_route_backward", "llmint8_expert_plan", "llmint8_experts_gated",
+                     "llmint8_experts_gated_backward", "llmint8_experts_matmul",
+                     "llmint8_experts_matmul_backward"):
             getattr(L, name).restype = C.c_int
         _lib = L
     return _lib
@@ -863,3 +895,316 @@ def llmint8_gated_backward(dH: torch.Tensor, X, Wg: torch.Tensor, Wu: torch.Tens
             Wu.data_ptr(), ldw, C.byref(g), C.byref(u), act, dt, _address(dX), lddx, _address(dWg),
             _address(dWu), lddw, ws, nb)
     return dX, dWg, dWu
+
+
+# ---- routed feed-forward layers ------------------------------------------------------
+# A router sends each token to k of E experts. As above, autograd does not see the calls.
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_LOGIT_TYPES = {**_DTYPES, torch.float32: LLMINT8_FP32}
+
+
+class ExpertPlan(NamedTuple):
+    """The (token, expert) pairs in the experts' order, int32: expert e has the rows
+    offsets[e] .. offsets[e + 1] - 1 (offsets [E + 1]); order [M k] is the pair i k + j of each
+    row, -1 behind the last; places [M, k] the row of each pair, -1 where it has none."""
+    offsets: torch.Tensor
+    order: torch.Tensor
+    places: torch.Tensor
+
+
+def _logits(logits) -> int:
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if logits.dtype not in _LOGIT_TYPES:
+        raise TypeError("logits must be torch.float16, torch.bfloat16 or torch.float32, got "
+                        f"{logits.dtype}")
+    return _matrix(logits, "logits", logits)
+
+
+def _route_opts(logits, scores, bias, groups, top_groups, group_best, renormalize, scale):
+    if scores not in _SCORES:
+        raise ValueError(f"scores is 'softmax' or 'sigmoid', got {scores!r}")
+    E = logits.shape[1]
+    b = None if bias is None else _vector(bias, "bias", torch.float32, E, logits)
+    return C.byref(RouteOpts(C.sizeof(RouteOpts), _SCORES[scores], bool(renormalize), scale, groups,
+                             groups if top_groups is None else top_groups, group_best, b))
+
+
+def _table(t, name: str, dtype, shape, like: torch.Tensor) -> int:
+    """The address of a contiguous matrix of this type and shape on like's device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.get_device() == like.get_device()):
+        _need(t, name, dtype, len(shape))
+        _need_shape(t, name, shape, contiguous=True)
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    return t.data_ptr()
+
+
+def llmint8_route(logits: torch.Tensor, k: int, *, scores: str = "softmax",
+                  bias: torch.Tensor | None = None, groups: int = 1,
+                  top_groups: int | None = None, group_best: int = 1, renormalize: bool = False,
+                  scale: float = 1.0):
+    """The k experts of each token: fp16, bf16 or fp32 logits [M, E] -> (ids int32 [M, k],
+    weights fp32 [M, k]).
+
+    scores is "softmax" (over the row) or "sigmoid". The k largest of score + bias (fp32 [E])
+    are chosen, ties to the lower index, in falling order; with groups > 1 out of the top_groups
+    best of `groups` equal runs of experts, a run's value being the sum of its group_best (1 or 2)
+    largest. weights are the scores of the chosen, divided by their sum with `renormalize`, times
+    `scale`. An expert whose logit is -inf or NaN is out: where fewer than k are left, the id is
+    -1 and the weight 0."""
+    ld = _logits(logits)
+    M, E = logits.shape
+    if not 1 <= k <= min(E, 64):
+        raise ValueError(f"k must be from 1 to {min(E, 64)}, got {k}")
+    if groups < 1 or E % groups:
+        raise ValueError(f"groups must divide the {E} experts, got {groups}")
+    opts = _route_opts(logits, scores, bias, groups, top_groups, group_best, renormalize, scale)
+    ids = torch.empty((M, k), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((M, k), dtype=torch.float32, device=logits.device)
+    _launch(lib().llmint8_route, logits, logits.data_ptr(), M, E, ld, _LOGIT_TYPES[logits.dtype],
+            k, opts, ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+def llmint8_route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, *,
+                           scores: str = "softmax", renormalize: bool = False, scale: float = 1.0,
+                           dlogits=None) -> torch.Tensor:
+    """The logits' gradient [M, E] (of their type) from dweights fp32 [M, k] and the ids of
+    llmint8_route; scores, renormalize and scale as there. The choice has no gradient."""
+    ld = _logits(logits)
+    M, E = logits.shape
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be [M, k]")
+    k = ids.shape[1]
+    i = _table(ids, "ids", torch.int32, (M, k), logits)
+    d = _table(dweights, "dweights", torch.float32, (M, k), logits)
+    opts = _route_opts(logits, scores, None, 1, None, 1, renormalize, scale)
+    dlogits, ldd = _out(dlogits, "dlogits", logits, (M, E))
+    _launch(lib().llmint8_route_backward, logits, d, logits.data_ptr(), M, E, ld,
+            _LOGIT_TYPES[logits.dtype], k, i, opts, dlogits.data_ptr(), ldd)
+    return dlogits
+
+
+def llmint8_expert_plan(ids: torch.Tensor, experts: int) -> ExpertPlan:
+    """The experts' order of the pairs that ids int32 [M, k] name (ids outside 0 .. experts - 1:
+    none). It serves every call on these ids, the backward ones too."""
+    _need(ids, "ids", torch.int32, 2)
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    M, k = ids.shape
+    # one allocation: the parts begin at multiples of 16 bytes
+    a, b = (experts + 4) // 4 * 4, (M * k + 3) // 4 * 4
+    held = torch.empty((a + 2 * b,), dtype=torch.int32, device=ids.device)
+    plan = ExpertPlan(held[:experts + 1], held[a:a + M * k],
+                      held[a + b:a + b + M * k].view(M, k))
+    at = held.data_ptr()
+    _launch(lib().llmint8_expert_plan, ids, ids.data_ptr(), M, k, experts, at, at + 4 * a,
+            at + 4 * (a + b))
+    return plan
+
+
+def _rows(plan, like: torch.Tensor, M: int | None = None) -> tuple:
+    """(the C view of a plan, its tokens, experts and choices of a token)"""
+    if not (isinstance(plan, tuple) and len(plan) == 3
+            and all(isinstance(t, torch.Tensor) for t in plan)):
+        raise TypeError("plan must be an ExpertPlan")
+    offsets, order, places = plan
+    if places.dim() != 2:
+        raise ValueError("plan.places must be [M, k]")
+    tokens, k = places.shape
+    if M is not None and tokens != M:
+        raise ValueError(f"the plan is of {tokens} tokens, not {M}")
+    E = offsets.numel() - 1
+    return C.byref(ExpertRows(_vector(offsets, "plan.offsets", torch.int32, E + 1, like),
+                              _vector(order, "plan.order", torch.int32, tokens * k, like),
+                              _table(places, "plan.places", torch.int32, (tokens, k), like), E,
+                              k)), tokens, E, k
+
+
+def _expert_weights(W, name: str, like: torch.Tensor, shape) -> tuple:
+    """(row stride, stride from expert to expert) of weights [E, rows, columns]."""
+    if not isinstance(W, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not (W.dtype is like.dtype and W.shape == shape and W.get_device() == like.get_device()
+            and W.is_contiguous()):
+        _need(W, name, like.dtype, 3)
+        _need_shape(W, name, shape)
+        if W.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}, got {W.device}")
+        if W.numel() == 0:
+            raise ValueError(f"{name} is empty ({tuple(W.shape)}); every dimension must be >= 1")
+    se, ld, s1 = W.stride()
+    E, rows, cols = shape
+    if s1 != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    ld = ld if rows > 1 else cols
+    return ld, se if E > 1 else rows * ld
+
+
+def _gate_experts(Wg, Wu, like: torch.Tensor, shape) -> tuple:
+    strides = _expert_weights(Wg, "Wg", like, shape)
+    if _expert_weights(Wu, "Wu", like, shape) != strides:
+        raise ValueError("Wg and Wu must have the same strides")
+    return strides
+
+
+def _out_experts(t, name: str, like: torch.Tensor, shape) -> tuple:
+    if t is None:
+        return like.new_empty(shape), shape[2], shape[1] * shape[2]
+    return t, *_expert_weights(t, name, like, shape)
+
+
+def _last_dims(W, name: str) -> tuple:
+    if not isinstance(W, torch.Tensor) or W.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions")
+    return W.shape[1:]
+
+
+def _experts_workspace(name: str, workspace, sizes, like: torch.Tensor):
+    need = getattr(lib(), f"llmint8_experts_{name}_workspace_size")(*sizes)
+    return _workspace(workspace, need, like)
+
+
+def llmint8_experts_gated_workspace_size(M: int, K: int, N: int, E: int, k: int) -> int:
+    return int(lib().llmint8_experts_gated_workspace_size(M, K, N, E, k))
+
+
+def llmint8_experts_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, plan: ExpertPlan, *,
+                          weights: torch.Tensor | None = None, activation: str = "silu",
+                          save: str = "none", H=None, workspace=None):
+    """The experts' gated blocks, H[r] = w act(x Wg_e) * (x Wu_e) for every row r of the plan:
+    fp16 or bf16 X [M, K], Wg and Wu [E, K, N], weights fp32 [M, k] (none: 1) -> H [M k, N].
+
+    Rows behind plan.offsets[E] are left as they were (uninitialized in an H made here). save
+    "full" returns (H, G, U) with the pre-activations in 16 bits, for
+    llmint8_experts_gated_backward."""
+    dt = _dtype_of(X, "X")
+    ldx = _matrix(X, "X", X)
+    M, K = X.shape
+    rows, _, E, k = _rows(plan, X, M)
+    N = _last_dims(Wg, "Wg")[1]
+    ldw, sw = _gate_experts(Wg, Wu, X, (E, K, N))
+    act = _activation(activation)
+    if save not in ("none", "full"):
+        raise ValueError(f"save is 'none' or 'full', got {save!r}")
+    w = None if weights is None else _table(weights, "weights", torch.float32, (M, k), X)
+    H, ldh = _out(H, "H", X, (M * k, N))
+    G = U = None
+    if save == "full":
+        G, U = X.new_empty((M * k, N)), X.new_empty((M * k, N))
+    ws, nb, keep = _experts_workspace("gated", workspace, (M, K, N, E, k), X)
+    _launch(lib().llmint8_experts_gated, X, X.data_ptr(), M, K, ldx, Wg.data_ptr(), Wu.data_ptr(),
+            ldw, sw, N, rows, w, act, dt, H.data_ptr(), ldh, _address(G), _address(U), N, ws, nb)
+    return H if save == "none" else (H, G, U)
+
+
+def llmint8_experts_gated_backward_workspace_size(M: int, K: int, N: int, E: int, k: int) -> int:
+    return int(lib().llmint8_experts_gated_backward_workspace_size(M, K, N, E, k))
+
+
+def llmint8_experts_gated_backward(dH: torch.Tensor, X: torch.Tensor | None, Wg: torch.Tensor,
+                                   Wu: torch.Tensor, G: torch.Tensor, U: torch.Tensor,
+                                   plan: ExpertPlan, *, weights: torch.Tensor | None = None,
+                                   activation: str = "silu", need_dX: bool = True,
+                                   need_dW: bool = True, need_dweights: bool = True, dX=None,
+                                   dWg=None, dWu=None, dweights=None, workspace=None):
+    """Gradients of llmint8_experts_gated from dH [M k, N]: (dX [M, K], dWg [E, K, N],
+    dWu [E, K, N], dweights fp32 [M, k]), None where not needed. X may be None without need_dW."""
+    dt = _dtype_of(dH, "dH")
+    lddh = _matrix(dH, "dH", dH)
+    rows, M, E, k = _rows(plan, dH)
+    K, N = _last_dims(Wg, "Wg")
+    _need_shape(dH, "dH", (M * k, N))
+    ldw, sw = _gate_experts(Wg, Wu, dH, (E, K, N))
+    act = _activation(activation)
+    ldx = K
+    if need_dW:
+        if X is None:
+            raise ValueError("dWg and dWu need X")
+        ldx = _matrix(X, "X", dH, (M, K))
+    if not (need_dX or need_dW or need_dweights):
+        raise ValueError("no gradient is asked for")
+    ldz = _matrix(G, "G", dH, (M * k, N))
+    if _matrix(U, "U", dH, (M * k, N)) != ldz:
+        raise ValueError("G and U must have the same row stride")
+    w = None if weights is None else _table(weights, "weights", torch.float32, (M, k), dH)
+    dX, lddx = _out(dX, "dX", dH, (M, K)) if need_dX else (None, 0)
+    lddw = sdw = 0
+    if need_dW:
+        dWg, lddw, sdw = _out_experts(dWg, "dWg", dH, (E, K, N))
+        dWu, *other = _out_experts(dWu, "dWu", dH, (E, K, N))
+        if other != [lddw, sdw]:
+            raise ValueError("dWg and dWu must have the same strides")
+    else:
+        dWg = dWu = None
+    if not need_dweights:
+        dweights = None
+    elif dweights is None:
+        dweights = torch.empty((M, k), dtype=torch.float32, device=dH.device)
+    else:
+        _table(dweights, "dweights", torch.float32, (M, k), dH)
+    ws, nb, keep = _experts_workspace("gated_backward", workspace, (M, K, N, E, k), dH)
+    _launch(lib().llmint8_experts_gated_backward, dH, dH.data_ptr(), M, N, lddh,
+            X.data_ptr() if need_dW else None, K, ldx, Wg.data_ptr(), Wu.data_ptr(), ldw, sw,
+            G.data_ptr(), U.data_ptr(), ldz, rows, w, act, dt, _address(dX), lddx, _address(dWg),
+            _address(dWu), lddw, sdw, _address(dweights), ws, nb)
+    return dX, dWg, dWu, dweights
+
+
+def llmint8_experts_matmul_workspace_size(M: int, K: int, N: int, E: int, k: int) -> int:
+    return int(lib().llmint8_experts_matmul_workspace_size(M, K, N, E, k))
+
+
+def llmint8_experts_matmul(H: torch.Tensor, Wd: torch.Tensor, plan: ExpertPlan, *,
+                           residual: torch.Tensor | None = None, Y=None,
+                           workspace=None) -> torch.Tensor:
+    """The experts' second product, summed over each token's experts: fp16 or bf16
+    H [M k, N] in the plan's order, Wd [E, N, K] -> Y [M, K] = residual + sum of H[r] Wd_e."""
+    dt = _dtype_of(H, "H")
+    ldh = _matrix(H, "H", H)
+    rows, M, E, k = _rows(plan, H)
+    N, K = _last_dims(Wd, "Wd")
+    _need_shape(H, "H", (M * k, N))
+    ldw, sw = _expert_weights(Wd, "Wd", H, (E, N, K))
+    r, ldr = None, 0
+    if residual is not None:
+        ldr, r = _matrix(residual, "residual", H, (M, K)), residual.data_ptr()
+    Y, ldy = _out(Y, "Y", H, (M, K))
+    ws, nb, keep = _experts_workspace("matmul", workspace, (M, K, N, E, k), H)
+    _launch(lib().llmint8_experts_matmul, H, H.data_ptr(), M, N, ldh, Wd.data_ptr(), ldw, sw, K,
+            rows, r, ldr, dt, Y.data_ptr(), ldy, ws, nb)
+    return Y
+
+
+def llmint8_experts_matmul_backward_workspace_size(M: int, K: int, N: int, E: int, k: int) -> int:
+    return int(lib().llmint8_experts_matmul_backward_workspace_size(M, K, N, E, k))
+
+
+def llmint8_experts_matmul_backward(dY: torch.Tensor, H: torch.Tensor | None, Wd: torch.Tensor,
+                                    plan: ExpertPlan, *, need_dH: bool = True,
+                                    need_dW: bool = True, dH=None, dWd=None, workspace=None):
+    """Gradients of llmint8_experts_matmul from dY [M, K]: (dH [M k, N], dWd [E, N, K]), None
+    where not needed (the residual's gradient is dY). H may be None without need_dW. Rows of dH
+    behind the plan's last are left as they were."""
+    dt = _dtype_of(dY, "dY")
+    lddy = _matrix(dY, "dY", dY)
+    M, K = dY.shape
+    rows, _, E, k = _rows(plan, dY, M)
+    N = _last_dims(Wd, "Wd")[0]
+    ldw, sw = _expert_weights(Wd, "Wd", dY, (E, N, K))
+    if not (need_dH or need_dW):
+        raise ValueError("no gradient is asked for")
+    ldh = N
+    if need_dW:
+        if H is None:
+            raise ValueError("dWd needs H")
+        ldh = _matrix(H, "H", dY, (M * k, N))
+    dH, lddh = _out(dH, "dH", dY, (M * k, N)) if need_dH else (None, 0)
+    dWd, lddw, sdw = _out_experts(dWd, "dWd", dY, (E, N, K)) if need_dW else (None, 0, 0)
+    ws, nb, keep = _experts_workspace("matmul_backward", workspace, (M, K, N, E, k), dY)
+    _launch(lib().llmint8_experts_matmul_backward, dY, dY.data_ptr(), M, K, lddy,
+            H.data_ptr() if need_dW else None, N, ldh, Wd.data_ptr(), ldw, sw, rows, dt,
+            _address(dH), lddh, _address(dWd), lddw, sdw, ws, nb)
+    return dH, dWd

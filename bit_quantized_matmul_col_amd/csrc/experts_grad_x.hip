@@ -1,0 +1,14 @@
+// Rows times the transposed weights: dH, and the rows of dX as one reduction of two segments.
+#include "experts_rows.hpp"
+
+namespace llmint8 {
+
+hipError_t launch_expert_grad_x(int dtype, const FfnGemm &a, const Pairs &p, int64_t bstride,
+                            int tile, hipStream_t s) {
+  using namespace ffn;
+  return dtype == LLMINT8_FP16
+             ? launch_rows_order<Half, Lay::RowK, Lay::RowK, false>(a, p, bstride, tile, s)
+             : launch_rows_order<Bfloat, Lay::RowK, Lay::RowK, false>(a, p, bstride, tile, s);
+}
+
+}  // namespace llmint8

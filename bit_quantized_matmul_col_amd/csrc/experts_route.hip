@@ -1,0 +1,403 @@
+// The router: which experts a token's row of logits chooses and with what weights, the
+// gradient of the logits, and the order of the (token, expert) pairs by expert.
+//
+// A wave has one row, lane l its experts l, l + 64, ... in registers.
+//
+// Selection. An expert whose logit is -infinity or NaN is out; +infinity counts as the largest
+// fp32 value. The value that experts are chosen by is the score (softmax or logistic) plus the
+// bias, in 64 bits: two scores close to each other fall the same way in any careful
+// implementation, where fp32 would leave their order to the rounding of an exponential. Without a
+// bias, and without sums of two scores for a group, the logits have the scores' order and no
+// exponential is needed. Values are turned into 64-bit integers of the same order; a step of
+// the top-k is a wave-wide maximum of the upper words (DPP moves, no LDS), a ballot of
+// who holds it, and the lower words or the indexes only where several lanes do.
+//
+// Weights and gradients in fp32; a renormalized weight is a softmax over the chosen logits (or
+// over the logarithms of their logistic scores), which has no 0 / 0 however small the scores.
+//
+// What bounds it: for few rows the launch and the k dependent steps (about 0.2 us each); for
+// many the instructions of the selection, not the 4 bytes a logit.
+#include "experts.hpp"
+#include "llmint8.h"
+
+namespace llmint8 {
+
+namespace {
+
+constexpr int kRows = 4;  // waves, and rows, of a block
+constexpr float kTop = 3.4028234663852886e38f;
+constexpr float kInf = __builtin_inff();
+
+template <int CTRL, int ROWS>
+__device__ inline uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+}
+__device__ inline uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// The largest of the wave's values, known to be uniform.
+__device__ inline uint32_t wave_umax(uint32_t v) {
+  v = umax(v, dpp<0x111, 0xf>(v));  // row_shr:1, 2, 4, 8
+  v = umax(v, dpp<0x112, 0xf>(v));
+  v = umax(v, dpp<0x114, 0xf>(v));
+  v = umax(v, dpp<0x118, 0xf>(v));
+  v = umax(v, dpp<0x142, 0xa>(v));  // row_bcast:15, 31
+  v = umax(v, dpp<0x143, 0xc>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+template <class F>
+__device__ inline F wave_add(F v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+  return v;
+}
+
+// Order-preserving integers; 0 is below every number.
+__device__ inline uint64_t ordered(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 to 0
+  return b >> 63 ? ~b : b | 1ull << 63;
+}
+
+__device__ inline float load_logit(const void *p, int64_t i, int dtype) {
+  if (dtype == 2) return ((const float *)p)[i];
+  const uint16_t h = ((const uint16_t *)p)[i];
+  return dtype == LLMINT8_FP16 ? h2f(h) : __builtin_bit_cast(float, (uint32_t)h << 16);
+}
+
+__device__ inline float log_logistic(float x) {
+  return __builtin_fminf(x, 0.f) - log1pf(expf(-__builtin_fabsf(x)));
+}
+
+// A row's logits: x[v] of expert lane + 64 v, -infinity where it is out or past the last.
+template <int V>
+__device__ inline void load_row(const Route &r, int64_t row, int lane, float *x) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = lane + 64 * v;
+    const float l = e < r.E ? load_logit(r.logits, row * r.ld + e, r.dtype) : -kInf;
+    x[v] = l > -kInf ? __builtin_fminf(l, kTop) : -kInf;  // a NaN compares false
+  }
+}
+
+// The chosen experts' weights before the scale: lane j has the logit c of slot j, or -infinity;
+// x the row.
+template <int V>
+__device__ inline float mix(const Route &r, const float *x, float c) {
+  const bool has = c > -kInf;
+  if (r.sigmoid && !r.renorm) return has ? 1.f / (1.f + expf(-c)) : 0.f;
+  if (r.renorm) {
+    const float z = !has ? -kInf : r.sigmoid ? log_logistic(c) : c;
+    const float top = wave_max(z);
+    const float p = has ? expf(z - top) : 0.f;
+    const float sum = wave_add(p);
+    return has ? p / sum : 0.f;
+  }
+  float top = -kInf;
+#pragma unroll
+  for (int v = 0; v < V; ++v) top = __builtin_fmaxf(top, x[v]);
+  top = wave_max(top);
+  float sum = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) sum += x[v] > -kInf ? expf(x[v] - top) : 0.f;
+  sum = wave_add(sum);
+  return has ? expf(c - top) / sum : 0.f;
+}
+
+template <int V>
+__global__ __launch_bounds__(64 * kRows) void k_route(Route r, int32_t *ids, float *weights) {
+  extern __shared__ double values[];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row = (int64_t)blockIdx.x * kRows + wv;
+  if (row >= r.M) return;  // no barrier below: a wave uses its own part of `values`
+  float x[V];
+  load_row<V>(r, row, lane, x);
+
+  // the values that experts are chosen by
+  double val[V];
+  if (!r.bias && r.group_best == 1) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) val[v] = x[v];
+  } else {
+    if (r.sigmoid) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) val[v] = 1.0 / (1.0 + exp(-(double)x[v]));
+    } else {
+      float top = -kInf;
+#pragma unroll
+      for (int v = 0; v < V; ++v) top = __builtin_fmaxf(top, x[v]);
+      top = wave_max(top);
+      double sum = 0.0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        val[v] = x[v] > -kInf ? exp((double)x[v] - (double)top) : 0.0;
+        sum += val[v];
+      }
+      sum = wave_add(sum);
+#pragma unroll
+      for (int v = 0; v < V; ++v) val[v] = sum > 0.0 ? val[v] / sum : 0.0;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = lane + 64 * v;
+      if (r.bias && e < r.E) val[v] += (double)r.bias[e];
+    }
+  }
+  uint64_t key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    key[v] = x[v] > -kInf && val[v] > -(double)kInf ? ordered(val[v]) : 0;
+
+  if (r.groups > 1) {
+    // lane g takes group g: its value, then how many groups come before it
+    double *const mine = values + (size_t)wv * r.E;
+    const int each = r.E / r.groups;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (lane + 64 * v < r.E) mine[lane + 64 * v] = key[v] ? val[v] : -(double)kInf;
+    __builtin_amdgcn_wave_barrier();
+    double best = -(double)kInf, second = best;
+    if (lane < r.groups)
+      for (int i = 0; i < each; ++i) {
+        const double d = mine[lane * each + i];
+        second = d > best ? best : d > second ? d : second;
+        best = d > best ? d : best;
+      }
+    if (r.group_best == 2 && second > -(double)kInf) best += second;
+    int before = 0;
+    for (int g = 0; g < r.groups; ++g) {
+      const double o = __shfl(best, g, kWave);
+      before += o > best || (o == best && g < lane);
+    }
+    const uint64_t keep = __ballot(lane < r.groups && before < r.top_groups);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = lane + 64 * v;
+      if (e < r.E && !(keep >> (e / each) & 1)) key[v] = 0;
+    }
+  }
+
+  int id = -1;        // of slot `lane`
+  float c = -kInf;    // its logit
+  for (int j = 0; j < r.k; ++j) {
+    uint64_t best = key[0];
+    int bv = 0;
+    float bx = x[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v)
+      if (key[v] > best) best = key[v], bv = v, bx = x[v];  // the lower index of equals
+    const uint32_t hi = (uint32_t)(best >> 32), lo = (uint32_t)best;
+    const uint32_t top = wave_umax(hi);
+    if (top == 0) break;  // every number's upper word is positive: none is left
+    uint64_t who = __ballot(hi == top);
+    if (who & (who - 1)) {
+      const uint32_t low = wave_umax(hi == top ? lo : 0);
+      who = __ballot(hi == top && lo == low);
+      if (who & (who - 1)) {
+        const bool in = who >> lane & 1;
+        const uint32_t first = wave_umax(in ? ~(uint32_t)(lane + 64 * bv) : 0);
+        who = __ballot(in && ~(uint32_t)(lane + 64 * bv) == first);
+      }
+    }
+    const int win = __builtin_ctzll(who);
+    const int wb = __builtin_amdgcn_readlane(bv, win);
+    const float wx = __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, bx), win));
+    if (lane == j) id = win + 64 * wb, c = wx;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (lane == win && v == wb) key[v] = 0;
+  }
+  const float w = mix<V>(r, x, c) * r.scale;
+  if (lane < r.k) {
+    ids[row * r.k + lane] = id;
+    weights[row * r.k + lane] = id < 0 ? 0.f : w;
+  }
+}
+
+// With weights w (before the scale), d = scale dweights and s = logistic:
+//   softmax                 dx_e = p_e (d_e - sum_j p_j d_j), d_e = 0 where e is not chosen
+//   softmax, renormalized   dx_j = w_j (d_j - sum_i w_i d_i), of chosen experts alone
+//   sigmoid                 dx_j = d_j s(x_j) s(-x_j)
+//   sigmoid, renormalized   dx_j = w_j s(-x_j) (d_j - sum_i w_i d_i)
+// An expert named twice gets both slots' gradients, in the slots' order.
+template <int V>
+__global__ __launch_bounds__(64 * kRows) void k_route_backward(Route r, const int32_t *ids,
+                                                               const float *dweights, void *dl,
+                                                               int64_t ldd) {
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row = (int64_t)blockIdx.x * kRows + wv;
+  if (row >= r.M) return;
+  float x[V];
+  load_row<V>(r, row, lane, x);
+  int id = -1;
+  float c = -kInf, d = 0.f;
+  if (lane < r.k) {
+    id = ids[row * r.k + lane];
+    if (id < 0 || id >= r.E) {
+      id = -1;
+    } else {
+      const float l = load_logit(r.logits, row * r.ld + id, r.dtype);
+      if (l > -kInf) c = __builtin_fminf(l, kTop), d = dweights[row * r.k + lane] * r.scale;
+    }
+  }
+  const float w = mix<V>(r, x, c);
+  const float mean = r.sigmoid && !r.renorm ? 0.f : wave_add(w * d);
+  float g;
+  if (r.sigmoid)
+    g = w * (d - mean) / (1.f + expf(c > -kInf ? c : 0.f));
+  else
+    g = r.renorm ? w * (d - mean) : w * d;
+  if (!(c > -kInf)) g = 0.f;
+  float out[V];
+  if (r.sigmoid || r.renorm) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) out[v] = 0.f;
+  } else {
+    float top = -kInf;
+#pragma unroll
+    for (int v = 0; v < V; ++v) top = __builtin_fmaxf(top, x[v]);
+    top = wave_max(top);
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      out[v] = x[v] > -kInf ? expf(x[v] - top) : 0.f;
+      sum += out[v];
+    }
+    sum = wave_add(sum);
+#pragma unroll
+    for (int v = 0; v < V; ++v) out[v] = sum > 0.f ? -mean * (out[v] / sum) : 0.f;
+  }
+  for (int j = 0; j < r.k; ++j) {
+    const int e = __builtin_amdgcn_readlane(id, j);
+    const float gj =
+        __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, g), j));
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (lane + 64 * v == e) out[v] += gj;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = lane + 64 * v;
+    if (e >= r.E) continue;
+    if (r.dtype == 2)
+      ((float *)dl)[row * ldd + e] = out[v];
+    else
+      ((uint16_t *)dl)[row * ldd + e] = r.dtype == LLMINT8_FP16
+                                            ? f2h(out[v])
+                                            : __builtin_bit_cast(uint16_t, (__bf16)out[v]);
+  }
+}
+
+// Block e of 0 .. E writes expert e's part of the order: it counts the pairs of the experts
+// before e, which is where e's rows begin, and e's own in each wave's stretch of the pairs,
+// then goes through them once more and puts each at its place. So one launch does it, pairs
+// of an expert keep their order and no atomic decides anything; block E has the pairs without an
+// expert. Every block reads all ids twice, from L2: 65536 pairs of 256 experts are 131 MB of
+// such reads, 0.5 MB a CU.
+constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
+
+__global__ __launch_bounds__(kPlanThreads) void k_expert_plan(const int32_t *ids, int64_t pairs,
+                                                              int E, int32_t *offsets,
+                                                              int32_t *order, int32_t *places) {
+  __shared__ int before[kPlanWaves], own[kPlanWaves];
+  const int e = blockIdx.x, lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // wave wv has the pairs p0 .. p1 - 1, in steps of 256: 4 of a lane
+  const int64_t step = (pairs + 256 * kPlanWaves - 1) / (256 * kPlanWaves) * 256;
+  const int64_t p0 = wv * step, p1 = p0 + step < pairs ? p0 + step : pairs;
+  auto load = [&](int64_t p, int *id) {
+    if (p + 4 <= p1) {
+      const i32x4 v = *(const i32x4 *)(ids + p);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) id[q] = (uint32_t)v[q] < (uint32_t)E ? v[q] : E;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int v = p + q < p1 ? ids[p + q] : -2;
+        id[q] = p + q >= p1 ? E + 1 : (uint32_t)v < (uint32_t)E ? v : E;
+      }
+    }
+  };
+  int less = 0, same = 0;
+  for (int64_t p = p0 + 4 * lane; p < p1; p += 256) {
+    int id[4];
+    load(p, id);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) less += id[q] < e, same += id[q] == e;
+  }
+  less = wave_sum(less), same = wave_sum(same);
+  if (lane == 0) before[wv] = less, own[wv] = same;
+  __syncthreads();
+  int begin = 0, at = 0, count = 0;
+#pragma unroll
+  for (int i = 0; i < kPlanWaves; ++i) {
+    begin += before[i], count += own[i];
+    at += i < wv ? own[i] : 0;
+  }
+  if (threadIdx.x == 0) offsets[e] = begin;
+  if (count == 0) return;
+  at += begin;
+  const uint64_t lower = ((uint64_t)1 << lane) - 1;
+  for (int64_t q0 = p0; q0 < p1; q0 += 256) {
+    int id[4] = {E + 1, E + 1, E + 1, E + 1};
+    const int64_t p = q0 + 4 * lane;
+    if (p < p1) load(p, id);
+    int ahead = 0, all = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint64_t m = __ballot(id[q] == e);
+      ahead += __popcll(m & lower), all += __popcll(m);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (id[q] == e) {
+        const int r = at + ahead++;
+        places[p + q] = e < E ? r : -1;
+        order[r] = e < E ? (int32_t)(p + q) : -1;
+      }
+    at += all;
+  }
+}
+
+template <int V>
+struct Width {
+  static constexpr int value = V;  // logits a lane
+};
+template <class F>
+hipError_t with_width(int E, F f) {
+  if (E <= 64) return f(Width<1>());
+  if (E <= 128) return f(Width<2>());
+  if (E <= 256) return f(Width<4>());
+  if (E <= 512) return f(Width<8>());
+  return f(Width<16>());
+}
+
+}  // namespace
+
+hipError_t launch_route(const Route &r, int32_t *ids, float *weights, hipStream_t s) {
+  const size_t lds = r.groups > 1 ? (size_t)kRows * r.E * sizeof(double) : 0;
+  return with_width(r.E, [&](auto w) {
+    hipLaunchKernelGGL((k_route<decltype(w)::value>), dim3((unsigned)((r.M + kRows - 1) / kRows)),
+                       dim3(64 * kRows), lds, s, r, ids, weights);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_route_backward(const Route &r, const int32_t *ids, const float *dweights,
+                                 void *dlogits, int64_t ldd, hipStream_t s) {
+  return with_width(r.E, [&](auto w) {
+    hipLaunchKernelGGL((k_route_backward<decltype(w)::value>),
+                       dim3((unsigned)((r.M + kRows - 1) / kRows)), dim3(64 * kRows), 0, s, r, ids,
+                       dweights, dlogits, ldd);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_expert_plan(const int32_t *ids, int64_t pairs, int E, int32_t *offsets,
+                              int32_t *order, int32_t *places, hipStream_t s) {
+  hipLaunchKernelGGL(k_expert_plan, dim3((unsigned)(E + 1)), dim3(kPlanThreads), 0, s, ids, pairs,
+                     E, offsets, order, places);
+  return hipGetLastError();
+}
+
+}  // namespace llmint8

@@ -33,6 +33,15 @@ struct FfnGemm {
   int64_t ldzs;
   float *part;    // split reduction: partial sums [ksplit][outs or 2][M][N]
   int ksplit;
+  // products over the rows that a router sent to an expert (see experts.hpp): row i of
+  // the product is that of the pair pairs[i], and A's row is
+  //   pairs[i] / topk of a matrix of a_rows rows, or i where topk is 0.
+  const int32_t *pairs;
+  int topk;
+  int64_t a_rows;
+  const float *w;  // [pairs] what a gated row is multiplied by (null: nothing)
+  int64_t all_rows;  // rows of all experts, and of a plane of partial sums
+  int to_parts;      // the sums go to `part`, split or not
 };
 
 // Which kernel a product takes: square tiles of `tile` rows and columns (256 or

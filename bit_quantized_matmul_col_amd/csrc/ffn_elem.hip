@@ -10,45 +10,13 @@
 //   activation's        2048 x 4096 bf16, with the bias gradient 14.8 us (50 MB),
 //                       4096 x 11008 50 us (5.4 TB/s)
 //   join                2 parts of 2048 x 4096, residual 16 us (101 MB, 6.3 TB/s)
-#include "ffn_gemm.hpp"
+#include "ffn_rows.hpp"
 
 namespace llmint8 {
 
 namespace {
 
-using ffn::load_f8;
-
-constexpr int kThreads = 256;
-
-// A block covers cx chunks of 8 columns (a power of two, 8 to 256, so that the 4
-// lanes of a checkpoint block share a wave) and 256 / cx rows at a time; the
-// grid's second dimension strides over the rows.
-struct RowGrid {
-  int cx_log2;
-  dim3 grid;
-};
-
-RowGrid row_grid(int64_t M, int64_t N, int64_t max_rows) {
-  const int64_t chunks = (N + 7) / 8;
-  int lg = 3;
-  while (lg < 8 && ((int64_t)1 << lg) < chunks) ++lg;
-  const int64_t gx = (chunks + ((int64_t)1 << lg) - 1) >> lg, ry = kThreads >> lg;
-  int64_t gy = (M + ry - 1) / ry;
-  if (gy > max_rows) gy = max_rows;
-  return RowGrid{lg, dim3((unsigned)gx, (unsigned)gy)};
-}
-
-constexpr int64_t kMaxGridY = 65535;
-
-// Calls f(i, n, in) for the rows i and the first column n of this thread's
-// chunks; in is false for a chunk past N (its lanes still take part in shuffles).
-template <class F>
-__device__ inline void for_rows(int cx_log2, int64_t M, int64_t N, F f) {
-  const int t = threadIdx.x;
-  const int64_t n = (((int64_t)blockIdx.x << cx_log2) + (t & ((1 << cx_log2) - 1))) * 8;
-  const int64_t ry = kThreads >> cx_log2;
-  for (int64_t i = blockIdx.y * ry + (t >> cx_log2); i < M; i += gridDim.y * ry) f(i, n, n < N);
-}
+using namespace ffn_rows;
 
 // 8 entries of a saved matrix. The scale byte is shared by 4 lanes.
 template <class T, bool Q8>
@@ -175,22 +143,6 @@ constexpr int kJoinThreads = 1024;
 __global__ __launch_bounds__(kJoinThreads) void k_bias_join(BiasJoin j) {
   __shared__ float s[64 * 64];
   ffn::join_bias<kJoinThreads>(j, blockIdx.x, s);
-}
-
-// Sums of the parts s0, s0 + 1, ... of 8 columns, in the order of the parts; the
-// loads of four parts are in flight together.
-__device__ inline void join_parts(const float *p, int64_t stride, int parts, float *v) {
-  for (int s = 0; s < parts; s += 4) {
-    float x[4][8];
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (s + q < parts) load_f8(p + (s + q) * stride, x[q]);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (s + q < parts)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += x[q][e];
-  }
 }
 
 // Joins the partial sums of a split reduction and runs the epilogue.

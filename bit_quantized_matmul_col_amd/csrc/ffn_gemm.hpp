@@ -98,7 +98,7 @@ struct Count {
   static constexpr int value = N;
 };
 
-enum class Lay { RowK, ColK };
+enum class Lay { RowK, ColK, RowKAt };
 
 __device__ inline int clip31(int64_t bytes) {
   return (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff);
@@ -156,6 +156,42 @@ struct RowKTile {
     return *(const s16x8 *)(tile + r * PITCH + 16 * ((4 * ks + (lane >> 4)) ^ key(r)));
   }
 };
+
+// A RowKTile whose rows are anywhere in a matrix of less than 2^31 bytes: row r of the tile
+// is row at(r) of it, or zeros where that is negative.
+template <int ROWS, int NW>
+struct RowKAtTile : RowKTile<ROWS, NW> {
+  using Base = RowKTile<ROWS, NW>;
+  template <class At>
+  __device__ void init_at(int64_t ld, int64_t mat_rows, int64_t len, At at) {
+    this->bytes = (int)((mat_rows - 1) * ld + len) * 2;
+    const int lane = threadIdx.x & 63, wv = wave_id();
+#pragma unroll
+    for (int j = 0; j < Base::G; ++j) {
+      const int r = (wv + NW * j) * Base::RPI + lane / Base::CH;
+      const int c = (lane % Base::CH) ^ Base::key(r);
+      const int64_t row = at(r);
+      this->voff[j] = row < 0 ? kOob : (int)row * (int)ld * 2 + 16 * c;
+      this->chunk = 8 * c;
+    }
+  }
+};
+
+// The matrix row of row i of a routed product (see FfnGemm), -1 past its end or for a pair
+// that no plan can hold.
+__device__ inline int64_t routed_row(const FfnGemm &a, int64_t i) {
+  if (i >= a.M) return -1;
+  if (!a.topk) return i;
+  const int64_t row = (uint32_t)a.pairs[i] / (uint32_t)a.topk;
+  return row < a.a_rows ? row : -1;
+}
+
+// What a gated row is multiplied by.
+__device__ inline float routed_weight(const FfnGemm &a, int64_t i) {
+  if (!a.w) return 1.f;
+  const uint32_t p = (uint32_t)a.pairs[i];
+  return (int64_t)p < a.all_rows ? a.w[p] : 0.f;
+}
 
 // Transposed LDS read: the 16 lanes of a group address a 4 x 16 block of 16-bit
 // values, lane i the entries 4 (i % 4) .. + 3 of row i / 4, and lane i receives
@@ -273,8 +309,9 @@ __device__ inline void save8(void *z, int64_t ldz, uint8_t *zs, int64_t ldzs, in
   if (n % kCkptBlock == 0) zs[i * ldzs + n / kCkptBlock] = (uint8_t)byte;
 }
 
-// act(g) * u of 8 columns of one row, and g and u to their places.
-template <class T>
+// act(g) * u of 8 columns of one row, times the row's weight where the product is routed,
+// and g and u to their places.
+template <class T, bool ROUTED = false>
 __device__ inline void finish_gated(const FfnGemm &a, int64_t i, int64_t n, bool in, float *g,
                                     float *u) {
   if (a.z[0]) {
@@ -286,6 +323,11 @@ __device__ inline void finish_gated(const FfnGemm &a, int64_t i, int64_t n, bool
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[e] = act_of<decltype(tag)::value>(g[e]) * u[e];
   });
+  if constexpr (ROUTED) {
+    const float w = routed_weight(a, i);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] *= w;
+  }
   store8<T>(a.y[0] + i * a.ldy + n, g);
 }
 
@@ -348,13 +390,17 @@ template <int N, int NW>
 struct TileOf<Lay::ColK, N, NW> {
   using type = ColKTile<N, NW>;
 };
+template <int N, int NW>
+struct TileOf<Lay::RowKAt, N, NW> {
+  using type = RowKAtTile<N, NW>;
+};
 
 // One launch shape: operand orders, block tile, waves.
 template <class T_, Lay LA_, Lay LB_, bool GATED_, int BM_, int BN_, int NWM_, int NWN_, int NST_ = 2>
 struct Cfg {
   using T = T_;
   static constexpr Lay LA = LA_, LB = LB_;
-  static constexpr bool GATED = GATED_;
+  static constexpr bool GATED = GATED_, ROUTED = LA_ == Lay::RowKAt;
   static constexpr int BM = BM_, BN = BN_, NWM = NWM_, NWN = NWN_, NW = NWM * NWN;
   static constexpr int THREADS = 64 * NW;
   static constexpr int WM = BM / NWM, WN = BN / NWN, MI = WM / 16, NI = WN / 16;
@@ -404,7 +450,10 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, int col
 
   TA A;
   TB B;
-  A.init(a.lda, a.M - m0, a.K);
+  if constexpr (C::ROUTED)
+    A.init_at(a.lda, a.a_rows, a.K, [&](int r) { return routed_row(a, m0 + r); });
+  else
+    A.init(a.lda, a.M - m0, a.K);
   B.init(a.ldb, a.N - n0, a.K);
 
   f32x4 acc[MI * NI];
@@ -558,14 +607,14 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, int col
       float v[8], u[8];
       load_f8(slab + r * C::SLABP + c8, v);
       if constexpr (C::GATED) load_f8(slab + r * C::SLABP + C::WO + c8, u);
-      if (a.ksplit > 1) {
+      if (!C::ROUTED && a.ksplit > 1) {  // a routed product is not split in tiles
         if (in) {
           float *part = a.part + (((int64_t)split * (C::GATED ? 2 : a.outs) + out) * a.M + i) * a.N + n;
           store_f8(part, v);
           if constexpr (C::GATED) store_f8(part + a.M * a.N, u);
         }
       } else if constexpr (C::GATED) {
-        if (i < a.M) finish_gated<T>(a, i, n, in, v, u);  // the 4 lanes of a block together
+        if (i < a.M) finish_gated<T, C::ROUTED>(a, i, n, in, v, u);  // the 4 lanes of a block together
       } else if (in) {
         finish_forward<T>(a, out, i, n, v, bias, res[mi & 1][p]);
       }

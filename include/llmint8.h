@@ -410,6 +410,129 @@ int llmint8_gated_backward(const uint16_t *dH, int64_t M, int64_t N, int64_t ldd
                            int64_t lddx, uint16_t *dWg, uint16_t *dWu, int64_t lddw,
                            void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Routed feed-forward layers: a router sends each of M tokens to k of E experts, each a gated
+ * block with weights of its own. Rules as for the 16-bit operators above; E is at most 1024, k
+ * at most E and at most 64, M k below 2^30.
+ *
+ * llmint8_route: the experts of each token and their weights, from the router's logits.
+ *   logits   [M x E], leading dimension ld >= E, of `dtype` LLMINT8_FP16, _BF16 or _FP32 (no
+ *            alignment beyond the type's).
+ *   An expert whose logit is -infinity or NaN is out for that token: never chosen, and nothing
+ *   to a softmax's sum (a padded row holds -infinity throughout). +infinity counts as the largest
+ *   fp32 value. Scores: softmax over the row, or the logistic function of each logit.
+ *   Choice: the k largest of score + bias, ties to the lower index, in falling order. With
+ *   groups > 1 the experts are `groups` equal runs; a run's value is the sum of its group_best
+ *   (1 or 2) largest score + bias, and only the top_groups best runs take part. The order is
+ *   that of the values in 64 bits (of the logits themselves, without a bias and with group_best 1).
+ *   ids      [M x k] int32: experts, -1 where none is left.
+ *   weights  [M x k] fp32: the scores of the chosen (without the bias), divided by their sum with
+ *            `renormalize`, times `scale`; 0 where the id is -1.
+ *   opts     may be NULL: softmax, no bias, one group, not renormalized, scale 1.
+ * llmint8_route_backward: dlogits [M x E] (leading dimension ldd, of the logits' type) from
+ *   dweights [M x k] fp32; the choice itself has no gradient, nor has the bias. `opts` as in the
+ *   forward call (its bias and groups are not read). An id outside 0 .. E - 1 adds nothing.
+ */
+#define LLMINT8_FP32 2
+#define LLMINT8_SCORE_SOFTMAX 0
+#define LLMINT8_SCORE_SIGMOID 1
+typedef struct llmint8_route_opts {
+  size_t struct_size;
+  int scores;      /* LLMINT8_SCORE_* */
+  int renormalize; /* 0 or 1 */
+  float scale;
+  int groups, top_groups, group_best;
+  const float *bias; /* optional [E] */
+} llmint8_route_opts;
+int llmint8_route(const void *logits, int64_t M, int64_t E, int64_t ld, int dtype, int64_t k,
+                  const llmint8_route_opts *opts, int32_t *ids, float *weights, void *stream);
+int llmint8_route_backward(const float *dweights, const void *logits, int64_t M, int64_t E,
+                           int64_t ld, int dtype, int64_t k, const int32_t *ids,
+                           const llmint8_route_opts *opts, void *dlogits, int64_t ldd,
+                           void *stream);
+
+/*
+ * The (token, expert) pairs in the experts' order. Pair p = i k + j is token i's j-th choice.
+ *   offsets  [E + 1]: expert e has the rows offsets[e] .. offsets[e + 1] - 1.
+ *   order    [M k]: the pair of each row, an expert's pairs in rising order; -1 behind the last.
+ *   places   [M x k]: the row of each pair, -1 for an id outside 0 .. E - 1, which has none.
+ * llmint8_expert_plan fills the three from ids [M x k]; nothing depends on the order in which
+ * blocks run. The calls below take them in an llmint8_expert_rows, and check what they read from
+ * them against the buffers' sizes; a plan of other ids gives other results but stays within.
+ */
+typedef struct llmint8_expert_rows {
+  const int32_t *offsets;
+  const int32_t *order;
+  const int32_t *places;
+  int64_t E, k;
+} llmint8_expert_rows;
+int llmint8_expert_plan(const int32_t *ids, int64_t M, int64_t k, int64_t E, int32_t *offsets,
+                        int32_t *order, int32_t *places, void *stream);
+
+/*
+ * The experts' gated blocks: for the row r of the pair of token i and expert e
+ *   H[r] = w[pair] act(G[r]) * U[r],  G[r] = X[i] . Wg_e,  U[r] = X[i] . Wu_e.
+ *   X        [M x K]. Its first and last element lie less than 2 GiB apart, or ldx = K.
+ *   Wg, Wu   [E][K x N], leading dimension ldw, stride_w elements from one expert to the next.
+ *   weights  [M x k] fp32, or NULL: 1.
+ *   H        [M k x N], leading dimension ldh. Rows behind the plan's last are left as they were.
+ *   G, U     both NULL, or both [M k x N] with leading dimension ldz: the pre-activations.
+ *   workspace  llmint8_experts_gated_workspace_size bytes (may be 0: NULL then).
+ */
+size_t llmint8_experts_gated_workspace_size(int64_t M, int64_t K, int64_t N, int64_t E, int64_t k);
+int llmint8_experts_gated(const uint16_t *X, int64_t M, int64_t K, int64_t ldx,
+                          const uint16_t *Wg, const uint16_t *Wu, int64_t ldw, int64_t stride_w,
+                          int64_t N, const llmint8_expert_rows *rows, const float *weights,
+                          int activation, int dtype, uint16_t *H, int64_t ldh, uint16_t *G,
+                          uint16_t *U, int64_t ldz, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
+ * Gradients of llmint8_experts_gated: with d = w[pair] dH[r],
+ *   dG = d * U * act'(G) and dU = d * act(G) (rounded to 16 bits, the products' operands),
+ *   dX[i] = the sum over token i's rows of dG . Wg_e^T + dU . Wu_e^T (each row's rounded to 16
+ *           bits before the sum, which is fp32),
+ *   dWg_e = X_e^T . dG_e, dWu_e = X_e^T . dU_e over expert e's rows (zeros without any),
+ *   dweights[pair] = sum over n of dH[r] act(G[r]) U[r] (fp32; 0 without a row).
+ * dX, dweights and the pair dWg, dWu (leading dimension lddw, stride_dw elements from expert to
+ * expert) may be NULL; X is read for dWg and dWu, Wg and Wu for dX.
+ */
+size_t llmint8_experts_gated_backward_workspace_size(int64_t M, int64_t K, int64_t N, int64_t E,
+                                                     int64_t k);
+int llmint8_experts_gated_backward(const uint16_t *dH, int64_t M, int64_t N, int64_t lddh,
+                                   const uint16_t *X, int64_t K, int64_t ldx, const uint16_t *Wg,
+                                   const uint16_t *Wu, int64_t ldw, int64_t stride_w,
+                                   const uint16_t *G, const uint16_t *U, int64_t ldz,
+                                   const llmint8_expert_rows *rows, const float *weights,
+                                   int activation, int dtype, uint16_t *dX, int64_t lddx,
+                                   uint16_t *dWg, uint16_t *dWu, int64_t lddw, int64_t stride_dw,
+                                   float *dweights, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/*
+ * The experts' second product and the sum over each token's experts:
+ *   Y[i] = R[i] + sum over token i's rows r of H[r] . Wd_e,
+ * H [M k x N] in the plan's order, Wd [E][N x K], R and Y [M x K] (R may be NULL). The rows are
+ * summed in fp32 in the order of the token's choices; where experts have many rows, each
+ * product is rounded to 16 bits before.
+ * Gradients: dH[r] = dY[i] . Wd_e^T (rows behind the plan's last left as they were), dWd_e =
+ * H_e^T . dY_e; either may be NULL. R's gradient is dY itself.
+ */
+size_t llmint8_experts_matmul_workspace_size(int64_t M, int64_t K, int64_t N, int64_t E, int64_t k);
+int llmint8_experts_matmul(const uint16_t *H, int64_t M, int64_t N, int64_t ldh,
+                           const uint16_t *Wd, int64_t ldw, int64_t stride_w, int64_t K,
+                           const llmint8_expert_rows *rows, const uint16_t *residual, int64_t ldr,
+                           int dtype, uint16_t *Y, int64_t ldy, void *workspace,
+                           size_t workspace_bytes, void *stream);
+size_t llmint8_experts_matmul_backward_workspace_size(int64_t M, int64_t K, int64_t N, int64_t E,
+                                                      int64_t k);
+int llmint8_experts_matmul_backward(const uint16_t *dY, int64_t M, int64_t K, int64_t lddy,
+                                    const uint16_t *H, int64_t N, int64_t ldh, const uint16_t *Wd,
+                                    int64_t ldw, int64_t stride_w,
+                                    const llmint8_expert_rows *rows, int dtype, uint16_t *dH,
+                                    int64_t lddh, uint16_t *dWd, int64_t lddw, int64_t stride_dw,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *llmint8_status_string(int status);
 
