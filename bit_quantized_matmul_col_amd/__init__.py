@@ -152,6 +152,12 @@ def lib() -> C.CDLL:
                                              i64, p, sz, p]
         L.llmint8_experts_matmul_backward.argtypes = [p, i64, i64, i64, p, i64, i64, p, i64, i64,
                                                       p, i, p, i64, p, i64, i64, p, sz, p]
+        L.llmint8_quantize_blockwise_fp8.argtypes = [p, i64, i64, i64, i, p, p, p]
+        L.llmint8_quantize_rowblock_fp8.argtypes = [p, i64, i64, i64, i, p, p, i64, p]
+        L.llmint8_linear_blockwise_fp8.argtypes = [p, i64, i64, i64, p, p, i64, i64, i, p, p, i64,
+                                                   p, sz, p]
+        L.llmint8_linear_blockwise_fp8_workspace_size.argtypes = [i64, i64, i64]
+        L.llmint8_linear_blockwise_fp8_workspace_size.restype = sz
         for name in ("gated", "gated_backward", "matmul", "matmul_backward"):
             query = getattr(L, f"llmint8_experts_{name}_workspace_size")
             query.argtypes, query.restype = [i64] * 5, sz
@@ -167,7 +173,8 @@ def lib() -> C.CDLL:
                      "llmint8_gated", "llmint8_gated_backward", "llmint8_route",
                      "llmint8_route_backward", "llmint8_expert_plan", "llmint8_experts_gated",
                      "llmint8_experts_gated_backward", "llmint8_experts_matmul",
-                     "llmint8_experts_matmul_backward"):
+                     "llmint8_experts_matmul_backward", "llmint8_quantize_blockwise_fp8",
+                     "llmint8_quantize_rowblock_fp8", "llmint8_linear_blockwise_fp8"):
             getattr(L, name).restype = C.c_int
         _lib = L
     return _lib
@@ -1208,3 +1215,70 @@ def llmint8_experts_matmul_backward(dY: torch.Tensor, H: torch.Tensor | None, Wd
             H.data_ptr() if need_dW else None, N, ldh, Wd.data_ptr(), ldw, sw, rows, dt,
             _address(dH), lddh, _address(dWd), lddw, sdw, ws, nb)
     return dH, dWd
+
+
+# ---- block-scaled FP8 ----------------------------------------------------------------
+# E4M3 codes in blocks of 128 along the reduction that share a power-of-two scale 2^(byte - 127).
+
+FP8_BLOCK = 128
+
+
+def llmint8_quantize_blockwise_fp8(W: torch.Tensor):
+    """fp16 or bf16 W [K, N] -> (Wq8 uint8 E4M3 codes [N, K], scale bytes uint8
+    [ceil(N / 128), ceil(K / 128)]): 128 x 128 entries share a scale."""
+    dt = _dtype_of(W, "W")
+    ldw = _matrix(W, "W", W)
+    K, N = W.shape
+    Wq = torch.empty((N, K), dtype=torch.uint8, device=W.device)
+    sw = torch.empty((-(-N // FP8_BLOCK), -(-K // FP8_BLOCK)), dtype=torch.uint8, device=W.device)
+    _launch(lib().llmint8_quantize_blockwise_fp8, W, W.data_ptr(), K, N, ldw, dt, Wq.data_ptr(),
+            sw.data_ptr())
+    return Wq, sw
+
+
+def llmint8_quantize_rowblock_fp8(X: torch.Tensor):
+    """fp16 or bf16 X [M, K] -> (Xq8 uint8 E4M3 codes [M, K], scale bytes uint8
+    [M, ceil(K / 128)]): 128 entries of a row share a scale. This is how
+    llmint8_linear_blockwise_fp8 codes its X."""
+    dt = _dtype_of(X, "X")
+    ldx = _matrix(X, "X", X)
+    M, K = X.shape
+    Xq = torch.empty((M, K), dtype=torch.uint8, device=X.device)
+    pitch = -(-K // (4 * FP8_BLOCK)) * 4
+    sx = torch.empty((M, pitch), dtype=torch.uint8, device=X.device)
+    _launch(lib().llmint8_quantize_rowblock_fp8, X, X.data_ptr(), M, K, ldx, dt, Xq.data_ptr(),
+            sx.data_ptr(), pitch)
+    return Xq, sx[:, :-(-K // FP8_BLOCK)]
+
+
+def llmint8_linear_blockwise_fp8_workspace_size(M: int, K: int, N: int) -> int:
+    return int(lib().llmint8_linear_blockwise_fp8_workspace_size(M, K, N))
+
+
+def llmint8_linear_blockwise_fp8(X: torch.Tensor, Wq8: torch.Tensor, scales: torch.Tensor, *,
+                                 bias: torch.Tensor | None = None, Y=None,
+                                 workspace=None) -> torch.Tensor:
+    """Y = X W + bias in block-scaled FP8: fp16 or bf16 X [M, K], which the call codes by rows,
+    Wq8 [N, K] and scales from llmint8_quantize_blockwise_fp8 -> Y [M, N] of X's type."""
+    dt = _dtype_of(X, "X")
+    ldx = _matrix(X, "X", X)
+    M, K = X.shape
+    if not isinstance(Wq8, torch.Tensor) or Wq8.dim() != 2:
+        raise ValueError("Wq8 must be contiguous [N, K]")
+    N = Wq8.shape[0]
+    w = _table(Wq8, "Wq8", torch.uint8, (N, K), X)
+    blocks = (-(-N // FP8_BLOCK), -(-K // FP8_BLOCK))
+    if not (isinstance(scales, torch.Tensor) and scales.dtype is torch.uint8
+            and scales.shape == blocks and scales.get_device() == X.get_device()):
+        _need(scales, "scales", torch.uint8, 2)
+        _need_shape(scales, "scales", blocks)
+        raise ValueError(f"scales must be on {X.device}, got {scales.device}")
+    lds = _ld(scales, "scales")
+    b = None if bias is None else _vector(bias, "bias", X.dtype, N, X)
+    Y, ldy = _out(Y, "Y", X, (M, N))
+    L = lib()
+    ws, nb, keep = _workspace(workspace,
+                              L.llmint8_linear_blockwise_fp8_workspace_size(M, K, N), X)
+    _launch(L.llmint8_linear_blockwise_fp8, X, X.data_ptr(), M, K, ldx, w, scales.data_ptr(), lds,
+            N, dt, b, Y.data_ptr(), ldy, ws, nb)
+    return Y

@@ -533,6 +533,37 @@ int llmint8_experts_matmul_backward(const uint16_t *dY, int64_t M, int64_t K, in
                                     int64_t lddh, uint16_t *dWd, int64_t lddw, int64_t stride_dw,
                                     void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Block-scaled FP8: E4M3 codes (the format of the FP8 layer above) in blocks of 128 along the
+ * reduction that share a power-of-two scale. The scale of a block is 2^e with the smallest e that
+ * has max |x| <= 448 2^e, at least -127, held as the byte e + 127; a code is the E4M3 value next to
+ * x 2^-e, ties to even, and the entry stands for value(code) 2^e. The division is exact, so codes
+ * and scales are bit-exact with this definition. A block with an infinity or a NaN takes the
+ * byte 255 and NaN codes and stands for NaN throughout.
+ * K is a multiple of 16 and at most 131072, N a multiple of 8.
+ *
+ * llmint8_quantize_blockwise_fp8: 16-bit W [K x N] -> Wq8 [N x K], blocks of 128 x 128 (those at the
+ *   ends smaller), scales [ceil(N / 128) x ceil(K / 128)].
+ * llmint8_quantize_rowblock_fp8: 16-bit X [M x K] -> Xq8 [M x K], blocks of 128 entries of a row,
+ *   scales [M x ld_scales] with ld_scales >= 4 ceil(K / 512): bytes past the row's last block up
+ *   to that width are written too.
+ * llmint8_linear_blockwise_fp8: Y = X8 . W8 [+ bias], X coded by rows as above (by the call), W as it
+ *   was coded (scales with leading dimension ld_scales >= ceil(K / 128), of any alignment). X, bias
+ *   and Y are of `dtype`. Products are exact, the sums fp32 (see the FP8 layer for what one MFMA
+ *   keeps); the result is rounded once.
+ *   workspace  llmint8_linear_blockwise_fp8_workspace_size(M, K, N) bytes (may be 0: NULL then).
+ */
+int llmint8_quantize_blockwise_fp8(const uint16_t *W, int64_t K, int64_t N, int64_t ldw, int dtype,
+                                   uint8_t *Wq8, uint8_t *scales, void *stream);
+int llmint8_quantize_rowblock_fp8(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, int dtype,
+                                  uint8_t *Xq8, uint8_t *scales, int64_t ld_scales, void *stream);
+size_t llmint8_linear_blockwise_fp8_workspace_size(int64_t M, int64_t K, int64_t N);
+int llmint8_linear_blockwise_fp8(const uint16_t *X, int64_t M, int64_t K, int64_t ldx,
+                                 const uint8_t *Wq8, const uint8_t *scales, int64_t ld_scales,
+                                 int64_t N, int dtype, const uint16_t *bias, uint16_t *Y,
+                                 int64_t ldy, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *llmint8_status_string(int status);
 
