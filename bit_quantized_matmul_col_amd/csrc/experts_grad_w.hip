@@ -1,48 +1,63 @@
 // dW_e = A_e^T B_e of every expert, A and B its rows: the reduction runs over the rows, as many
 // as the router sent, none at all for some (whose gradient is zeros).
-#include "experts_tile.hpp"
+#include "experts_core.hpp"
 
 namespace llmint8 {
 namespace ffn {
 
+struct ExpertGradArgs {
+  FfnGemm a;
+  const int32_t *offsets;
+  int64_t ystride;
+  int E, tiles_m, cols;  // experts, tile rows and tile columns of one
+};
+
 template <class C>
-__global__ __launch_bounds__(C::THREADS, 2) void k_expert_grad_w(FfnGemm a, const int32_t *offsets,
-                                                                int64_t rows, int64_t ystride,
-                                                                int tiles_m, int cols) {
+__global__ __launch_bounds__(C::THREADS, 2) void k_expert_grad_w(ExpertGradArgs args) {
   extern __shared__ u32x4 smem_v[];
-  const uint32_t per = (uint32_t)(tiles_m * cols), place = xcd_place(blockIdx.x, gridDim.x);
-  const int e = (int)(place / per);
-  // the tiles of one expert in consecutive places, ordered as in tile_at
-  constexpr uint32_t GM = gemm_detail::kGroupM;
-  const uint32_t v = place % per, first = v / (GM * cols) * GM, in = v % (GM * cols);
-  const uint32_t gm = tiles_m - first < GM ? tiles_m - first : GM;
-  const int tm = (int)(first + in % gm), tn = (int)(in / gm);
-  auto at = [&](int i) {
-    const int64_t o = offsets[i];
-    return o < 0 ? (int64_t)0 : o < rows ? o : rows;
+  // an expert's tiles one after the other, ordered as in tile_at
+  auto find = [&](const auto *k, uint32_t place, Job &j) {
+    constexpr uint32_t GM = gemm_detail::kGroupM;
+    const uint32_t cols = (uint32_t)k->cols, tiles_m = (uint32_t)k->tiles_m;
+    const uint32_t per = tiles_m * cols, v = place % per;
+    const int e = (int)(place / per);
+    const uint32_t g0 = v / (GM * cols) * GM, in = v % (GM * cols);
+    const uint32_t gm = tiles_m - g0 < GM ? tiles_m - g0 : GM;
+    const int64_t m0 = (int64_t)(g0 + in % gm) * C::BM;
+    int tn = (int)(in / gm);
+    const int tn1 = (int)((k->a.N + C::OUTN - 1) / C::OUTN), out = tn >= tn1;
+    if (out) tn -= tn1;
+    const int64_t n0 = (int64_t)tn * C::OUTN;
+    // by the scalar cache, which holds the offsets after the first tiles
+    const int32_t __attribute__((address_space(4))) *const off =
+        (const int32_t __attribute__((address_space(4))) *)k->offsets;
+    auto at = [&](int o) { return o < 0 ? 0 : o < k->a.all_rows ? o : (int)k->a.all_rows; };
+    const int64_t first = at(off[e]);
+    const int n = at(off[e + 1]) - (int)first;
+    j.a[0] = j.a[1] = (const uint8_t *)((const uint16_t *)k->a.a[0] + first * k->a.lda + m0);
+    j.b[0] = j.b[1] = (const uint8_t *)((const uint16_t *)(out ? k->a.b[1] : k->a.b[0]) +
+                                        first * k->a.ldb + n0);
+    j.K = n > 0 ? n : 0;
+    j.pairs = nullptr;
+    j.out = Job::Out{(out ? k->a.y[1] : k->a.y[0]) + e * k->ystride + m0 * k->a.ldy + n0, 0, 0,
+                     (int)(k->a.M - m0 < C::BM ? k->a.M - m0 : C::BM), (int)(k->a.N - n0)};
   };
-  const int64_t r0 = at(e), r1 = at(e + 1), m0 = (int64_t)tm * C::BM;
-  FfnGemm g = a;
-  g.a[0] = (const uint16_t *)a.a[0] + r0 * a.lda + m0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    g.b[i] = (const uint16_t *)a.b[i] + r0 * a.ldb;
-    g.y[i] = a.y[i] + e * ystride + m0 * a.ldy;
-  }
-  g.K = r1 > r0 ? r1 - r0 : 0;
-  g.M = a.M - m0 < C::BM ? a.M - m0 : C::BM;
-  ffn_tile<C>(g, 0, tn, 1, (uint8_t *)smem_v);
+  run_tiles<C, ExpertGradArgs>(args.a.lda, args.a.ldb, 1,
+                               (uint32_t)(args.E * args.tiles_m * args.cols), find,
+                               (uint8_t *)smem_v);
 }
 
 template <class C>
 hipError_t launch_grad_w_cfg(const FfnGemm &a, const Pairs &p, int64_t ystride, hipStream_t s) {
   auto *kern = k_expert_grad_w<C>;
-  hipError_t e = hipFuncSetAttribute((const void *)kern,
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
+  constexpr int LDS = tiles_lds<C>();
+  hipError_t e =
+      hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
   if (e != hipSuccess) return e;
   const int64_t tiles_m = (a.M + C::BM - 1) / C::BM, cols = (a.N + C::OUTN - 1) / C::OUTN * a.outs;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles_m * cols * p.E)), dim3(C::THREADS), C::LDS, s, a,
-                     p.offsets, p.rows(), ystride, (int)tiles_m, (int)cols);
+  const int64_t tiles = tiles_m * cols * p.E, room = kFfnCus * (C::BM == 256 ? 1 : 2);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles < room ? tiles : room)), dim3(C::THREADS), LDS, s,
+                     ExpertGradArgs{a, p.offsets, ystride, p.E, (int)tiles_m, (int)cols});
   return hipGetLastError();
 }
 

@@ -1,59 +1,74 @@
-// Products over the rows that a router sent to each expert, in square tiles: every tile is one
-// of ffn_gemm.hpp, of the rows of one expert. Tiles of 256 rows, whose last of an expert has
-// half of them where that is enough, or of 128.
+// Products over the rows that a router sent to each expert, in square tiles of 256 or 128 rows of
+// one expert.
 #pragma once
 
-#include "experts_tile.hpp"
+#include "experts_core.hpp"
 
 namespace llmint8 {
 namespace ffn {
 
-template <class C1, class C2>
-__global__ __launch_bounds__(C1::THREADS, 2) void k_expert_rows(FfnGemm a, const int32_t *offsets,
-                                                               int E, int64_t bstride, int cols) {
-  static_assert(C1::THREADS == C2::THREADS && C1::OUTN == C2::OUTN, "one launch");
+struct ExpertRowsArgs {
+  FfnGemm a;
+  const int32_t *offsets;
+  int64_t bstride;
+  int E, cols;  // experts, tile columns
+};
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS, 2) void k_expert_rows(ExpertRowsArgs args) {
   extern __shared__ u32x4 smem_v[];
-  ExpertTile t;
-  if (!expert_tile<C1::BM>(offsets, E, a.all_rows, cols, 1, gemm_detail::kGroupM, blockIdx.x,
-                           t))
-    return;
-  FfnGemm g = expert_product(a, t, bstride);
-  // what no such product has, known to the compiler
-  g.outs = g.ksplit = 1;
-  g.bias = g.residual = nullptr;
-  g.zs[0] = g.zs[1] = nullptr;
-  if constexpr (C1::GATED)
-    g.segs = 1;
-  else
-    g.act = LLMINT8_ACT_NONE, g.z[0] = nullptr;
-  if (C1::BM == C2::BM || t.rows > C2::BM)
-    ffn_tile<C1>(g, 0, t.tn, 1, (uint8_t *)smem_v);
-  else
-    ffn_tile<C2>(g, 0, t.tn, 1, (uint8_t *)smem_v);
+  ExpertTable table((uint8_t *)smem_v + tiles_lds<C>(), args.E);
+  table.fill<C::BM>(args.offsets, args.a.all_rows);
+  __syncthreads();
+  const uint32_t tiles = table.tiles() * (uint32_t)args.cols;
+  // The tiles of an expert in consecutive places, its tile rows in groups of 8, a group column
+  // by column, as in tile_at: neighbours share weights and rows, and the weights, which
+  // are most of what is read, leave HBM once.
+  auto find = [&](const auto *k, uint32_t place, Job &j) {
+    constexpr uint32_t GM = gemm_detail::kGroupM;
+    const uint32_t cols = (uint32_t)k->cols;
+    const int e = table.expert_of((int)(place / cols));
+    const uint32_t rows = (uint32_t)table.tile_rows(e);
+    const uint32_t v = place - (uint32_t)table.start(e) * cols;
+    const uint32_t g0 = v / (GM * cols) * GM, in = v % (GM * cols);
+    const uint32_t gm = rows - g0 < GM ? rows - g0 : GM;
+    const int64_t n0 = (int64_t)(in / gm) * C::OUTN;
+    ExpertTile t;
+    table.rows_of<C::BM>(e, (int)(g0 + in % gm), t);
+    const int64_t r = t.row0;
+    const int64_t b0 = t.expert * k->bstride + (C::LB == Lay::RowK ? n0 * k->a.ldb : n0);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      j.a[q] = (const uint8_t *)((const uint16_t *)k->a.a[q] + (k->a.topk ? 0 : r * k->a.lda));
+      j.b[q] = (const uint8_t *)((const uint16_t *)k->a.b[q] + b0);
+    }
+    j.K = (int)k->a.K;
+    j.pairs = k->a.pairs + r;
+    j.out = Job::Out{k->a.y[0] + r * k->a.ldy + n0, t.row0, (int)n0, t.rows, (int)(k->a.N - n0)};
+  };
+  run_tiles<C, ExpertRowsArgs>(args.a.lda, args.a.ldb, args.a.segs, tiles, find,
+                               (uint8_t *)smem_v);
 }
 
-template <class C1, class C2>
+template <class C>
 hipError_t launch_rows_cfg(const FfnGemm &a, const Pairs &p, int64_t bstride, hipStream_t s) {
-  auto *kern = k_expert_rows<C1, C2>;
-  constexpr int LDS = C1::LDS > C2::LDS ? C1::LDS : C2::LDS;
+  auto *kern = k_expert_rows<C>;
+  const int lds = tiles_lds<C>() + ExpertTable::bytes(p.E);
   hipError_t e =
-      hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
+      hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
-  const int64_t cols = (a.N + C1::OUTN - 1) / C1::OUTN;
-  const int64_t blocks = expert_tiles(a.M, p.E, C1::BM) * cols;
-  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(C1::THREADS), LDS, s, a, p.offsets, p.E,
-                     bstride, (int)cols);
+  const int64_t cols = (a.N + C::OUTN - 1) / C::OUTN, most = expert_tiles(a.M, p.E, C::BM) * cols;
+  const int64_t room = kFfnCus * (C::BM == 256 ? 1 : 2);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(most < room ? most : room)), dim3(C::THREADS), lds, s,
+                     ExpertRowsArgs{a, p.offsets, bstride, p.E, (int)cols});
   return hipGetLastError();
 }
 
 template <class T, Lay LA, Lay LB, bool GATED>
 hipError_t launch_rows_order(const FfnGemm &a, const Pairs &p, int64_t bstride, int tile,
                              hipStream_t s) {
-  using Wide = Cfg<T, LA, LB, GATED, 256, 256, 2, 4>;
-  using Half_ = Cfg<T, LA, LB, GATED, 128, 256, 2, 4>;
-  using Small = Cfg<T, LA, LB, GATED, 128, 128, 2, 2>;
-  return tile == 256 ? launch_rows_cfg<Wide, Half_>(a, p, bstride, s)
-                     : launch_rows_cfg<Small, Small>(a, p, bstride, s);
+  return tile == 256 ? launch_rows_cfg<Cfg<T, LA, LB, GATED, 256, 256, 2, 4>>(a, p, bstride, s)
+                     : launch_rows_cfg<Cfg<T, LA, LB, GATED, 128, 128, 2, 2>>(a, p, bstride, s);
 }
 
 }  // namespace ffn

@@ -13,9 +13,16 @@ __global__ __launch_bounds__(64 * kSkWaves, 1) void k_expert_skinny(FfnGemm a,
                                                                    const int32_t *offsets, int E,
                                                                    int64_t bstride, int cols) {
   extern __shared__ u32x4 smem_v[];
+  // The launch has blocks for the worst distribution of the rows; those behind the row groups
+  // that there are end here. All row groups, column by column: those of one expert share
+  // its weights in L2.
+  const uint32_t groups = count_tiles<16 * C::MT>(offsets, E, a.all_rows);
+  const uint32_t plane = groups * (uint32_t)cols, blocks = plane * (uint32_t)a.ksplit;
+  if (blockIdx.x >= blocks) return;
+  const uint32_t place = xcd_place(blockIdx.x, blocks);
   ExpertTile t;
-  // all row groups, column by column: those of one expert share its weights in L2
-  if (!expert_tile<16 * C::MT>(offsets, E, a.all_rows, cols, a.ksplit, 0, blockIdx.x, t)) return;
+  find_rows<16 * C::MT>(offsets, E, a.all_rows, (int)(place % plane % groups), t);
+  t.tn = (int)(place % plane / groups), t.part = (int)(place / plane);
   skinny_block<C>(expert_product(a, t, bstride), t.part, 0, (int64_t)t.tn * C::CB,
                   (uint8_t *)smem_v);
 }

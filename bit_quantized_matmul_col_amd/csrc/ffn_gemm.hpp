@@ -98,6 +98,7 @@ struct Count {
   static constexpr int value = N;
 };
 
+// RowKAt: RowK, from rows that need not be neighbours (experts_core.hpp).
 enum class Lay { RowK, ColK, RowKAt };
 
 __device__ inline int clip31(int64_t bytes) {
@@ -154,26 +155,6 @@ struct RowKTile {
   __device__ static s16x8 frag(const uint8_t *tile, int row0, int ks, int lane) {
     const int r = row0 + (lane & 15);
     return *(const s16x8 *)(tile + r * PITCH + 16 * ((4 * ks + (lane >> 4)) ^ key(r)));
-  }
-};
-
-// A RowKTile whose rows are anywhere in a matrix of less than 2^31 bytes: row r of the tile
-// is row at(r) of it, or zeros where that is negative.
-template <int ROWS, int NW>
-struct RowKAtTile : RowKTile<ROWS, NW> {
-  using Base = RowKTile<ROWS, NW>;
-  template <class At>
-  __device__ void init_at(int64_t ld, int64_t mat_rows, int64_t len, At at) {
-    this->bytes = (int)((mat_rows - 1) * ld + len) * 2;
-    const int lane = threadIdx.x & 63, wv = wave_id();
-#pragma unroll
-    for (int j = 0; j < Base::G; ++j) {
-      const int r = (wv + NW * j) * Base::RPI + lane / Base::CH;
-      const int c = (lane % Base::CH) ^ Base::key(r);
-      const int64_t row = at(r);
-      this->voff[j] = row < 0 ? kOob : (int)row * (int)ld * 2 + 16 * c;
-      this->chunk = 8 * c;
-    }
   }
 };
 
@@ -390,10 +371,6 @@ template <int N, int NW>
 struct TileOf<Lay::ColK, N, NW> {
   using type = ColKTile<N, NW>;
 };
-template <int N, int NW>
-struct TileOf<Lay::RowKAt, N, NW> {
-  using type = RowKAtTile<N, NW>;
-};
 
 // One launch shape: operand orders, block tile, waves.
 template <class T_, Lay LA_, Lay LB_, bool GATED_, int BM_, int BN_, int NWM_, int NWN_, int NST_ = 2>
@@ -450,10 +427,7 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, int col
 
   TA A;
   TB B;
-  if constexpr (C::ROUTED)
-    A.init_at(a.lda, a.a_rows, a.K, [&](int r) { return routed_row(a, m0 + r); });
-  else
-    A.init(a.lda, a.M - m0, a.K);
+  A.init(a.lda, a.M - m0, a.K);
   B.init(a.ldb, a.N - n0, a.K);
 
   f32x4 acc[MI * NI];
@@ -607,14 +581,14 @@ __device__ __forceinline__ void ffn_tile(const FfnGemm &a, uint32_t bid, int col
       float v[8], u[8];
       load_f8(slab + r * C::SLABP + c8, v);
       if constexpr (C::GATED) load_f8(slab + r * C::SLABP + C::WO + c8, u);
-      if (!C::ROUTED && a.ksplit > 1) {  // a routed product is not split in tiles
+      if (a.ksplit > 1) {
         if (in) {
           float *part = a.part + (((int64_t)split * (C::GATED ? 2 : a.outs) + out) * a.M + i) * a.N + n;
           store_f8(part, v);
           if constexpr (C::GATED) store_f8(part + a.M * a.N, u);
         }
       } else if constexpr (C::GATED) {
-        if (i < a.M) finish_gated<T, C::ROUTED>(a, i, n, in, v, u);  // the 4 lanes of a block together
+        if (i < a.M) finish_gated<T>(a, i, n, in, v, u);  // the 4 lanes of a block together
       } else if (in) {
         finish_forward<T>(a, out, i, n, v, bias, res[mi & 1][p]);
       }
