@@ -32,12 +32,11 @@ struct Fp8Gemm {
   FfnGemm out;  // M, N, y, ldy, bias, part, ksplit
 };
 
+// The few-row kernel with `cols` columns a block, X coded in it or not; or tiles of `tile` rows
+// and columns.
 struct Fp8Plan {
-  bool few;    // the few-row kernel: `cols` columns and `rows` rows a block, X coded in it or not
-  bool fused;
-  int tile;    // 256 or 128 otherwise
-  int ksplit;
-  int rows, cols;
+  bool few, fused;
+  int tile, ksplit, cols;
 };
 Fp8Plan fp8_plan(int64_t M, int64_t K, int64_t N);
 

@@ -5,23 +5,6 @@
 
 using namespace llmint8;
 
-namespace llmint8 {
-
-Fp8Plan fp8_plan(int64_t M, int64_t K, int64_t N) {
-  Fp8Plan p{false, false, 128, 1, 0, 0};
-  if (M <= 128) {
-    p.few = true, p.fused = M <= 16;
-    p.rows = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-    p.cols = N >= 16384 ? 64 : N >= 8192 ? 32 : 16;
-    return p;
-  }
-  const int64_t t256 = (M + 255) / 256 * ((N + 255) / 256);
-  if (t256 >= 200) p.tile = 256;
-  return p;
-}
-
-}  // namespace llmint8
-
 namespace {
 
 void check_sizes(Check &c, int64_t M, int64_t K, int64_t N) {

@@ -5,7 +5,7 @@
 // MFMA run along the reduction, a load of 16 bytes a lane covers 64 bytes of each of 16 columns,
 // and nothing is shared that LDS would save. It keeps D blocks of the reduction in flight
 // in registers; the waves of a block take the blocks of the reduction in turn, and their
-// sums meet in LDS in a fixed order. For up to 16 rows X comes in 16 bits and every wave codes
+// sums meet in LDS in a fixed order. For the fewest rows X comes in 16 bits and every wave codes
 // what it needs itself, which its loads of W leave time for, so that a token is one launch;
 // for more rows a pass has coded X before.
 #include "blockwise_math.hpp"
@@ -18,7 +18,7 @@ struct FewCfg {
   using T = T_;
   static constexpr int MT = MT_, NB = NB_, WAVES = WAVES_;  // row tiles, column tiles, waves
   static constexpr bool FUSED = FUSED_;
-  static constexpr int D = NB * MT >= 8 ? 2 : 4;  // blocks of the reduction in flight
+  static constexpr int D = NB * MT >= 8 || (FUSED && NB == 4) ? 2 : 4;  // blocks in flight
   static constexpr int CB = 16 * NB, THREADS = 64 * WAVES;
   static constexpr int REDP = CB + 4;  // fp32 pitch of the joined sums
   static constexpr int LDS = WAVES * 16 * MT * REDP * 4;
@@ -187,9 +187,8 @@ hipError_t launch_few_cols(const Fp8Gemm &a, int cols, hipStream_t s) {
 
 template <class T>
 hipError_t launch_few_type(const Fp8Gemm &a, const Fp8Plan &p, hipStream_t s) {
-  if (p.fused) return launch_few_cols<T, 1, true>(a, p.cols, s);
-  if (p.rows == 32) return launch_few_cols<T, 2, false>(a, p.cols, s);
-  return launch_few_cols<T, 4, false>(a, p.cols, s);
+  return p.fused ? launch_few_cols<T, 1, true>(a, p.cols, s)
+                 : launch_few_cols<T, 2, false>(a, p.cols, s);
 }
 
 }  // namespace fp8

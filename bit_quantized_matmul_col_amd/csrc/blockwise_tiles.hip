@@ -39,8 +39,10 @@ struct Fp8Cfg {
   static_assert(MI % 4 == 0 && WN <= kFp8Block, "a ring of four fragments; one scale a wave");
 };
 
+// Block bid of the tiles in tile columns col0 .. col0 + cols - 1.
 template <class C>
-__device__ __forceinline__ void fp8_tile(const Fp8Gemm &a, uint8_t *const smem) {
+__device__ __forceinline__ void fp8_tile(const Fp8Gemm &a, uint32_t bid, int col0, int cols,
+                                         uint8_t *const smem) {
   using T = typename C::T;
   constexpr int MI = C::MI, NI = C::NI, LPS = C::LPS, NST = C::NST;
   const int t = threadIdx.x, lane = t & 63, wv = wave_id();
@@ -48,8 +50,8 @@ __device__ __forceinline__ void fp8_tile(const Fp8Gemm &a, uint8_t *const smem) 
   const FfnGemm &o = a.out;
 
   int tm, tn, split;
-  tile_at(blockIdx.x, (uint32_t)((o.M + C::BM - 1) / C::BM), (uint32_t)((o.N + C::BN - 1) / C::BN),
-          o.ksplit, tm, tn, split);
+  tile_at(bid, (uint32_t)((o.M + C::BM - 1) / C::BM), (uint32_t)cols, o.ksplit, tm, tn, split);
+  tn += col0;
   const int64_t m0 = (int64_t)tm * C::BM, n0 = (int64_t)tn * C::BN;
   const int64_t half = a.K / 2;  // pairs of codes in a row
   const int nst = (int)((a.K + kFp8Block - 1) / kFp8Block);
@@ -229,31 +231,45 @@ __device__ __forceinline__ void fp8_tile(const Fp8Gemm &a, uint8_t *const smem) 
   }
 }
 
-template <class C>
-__global__ __launch_bounds__(C::THREADS, 2) void k_fp8_tiles(Fp8Gemm a) {
+// The last blocks take the C1 tiles of the tile columns before `cut`, the first ones the C2
+// tiles of the rest: half tiles where the last round would be nearly empty (see tail_cut).
+template <class C1, class C2>
+__global__ __launch_bounds__(C1::THREADS, 2) void k_fp8_tiles(Fp8Gemm a, int cut, int cols,
+                                                             uint32_t blocks1) {
+  static_assert(C1::THREADS == C2::THREADS && C1::BN == C2::BN, "one launch");
   extern __shared__ u32x4 smem_v[];
-  fp8_tile<C>(a, (uint8_t *)smem_v);
+  const uint32_t blocks2 = gridDim.x - blocks1;
+  if (blockIdx.x >= blocks2)
+    fp8_tile<C1>(a, blockIdx.x - blocks2, 0, cut, (uint8_t *)smem_v);
+  else
+    fp8_tile<C2>(a, blockIdx.x, cut, cols - cut, (uint8_t *)smem_v);
 }
 
-template <class C>
+template <class C1, class C2>
 hipError_t launch_cfg(const Fp8Gemm &a, hipStream_t s) {
-  auto *kern = k_fp8_tiles<C>;
-  const int64_t lds = C::lds(a.K);
+  auto *kern = k_fp8_tiles<C1, C2>;
+  const int64_t lds = C1::lds(a.K) > C2::lds(a.K) ? C1::lds(a.K) : C2::lds(a.K);
   hipError_t e = hipFuncSetAttribute((const void *)kern,
                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  const int64_t blocks = (a.out.M + C::BM - 1) / C::BM * ((a.out.N + C::BN - 1) / C::BN) *
-                         a.out.ksplit;
-  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(C::THREADS), (unsigned)lds, s, a);
+  const int64_t rows = (a.out.M + C1::BM - 1) / C1::BM, cols = (a.out.N + C1::BN - 1) / C1::BN;
+  const int64_t cut = C1::BM == C2::BM ? cols : tail_cut(rows, cols, a.out.ksplit);
+  const int64_t blocks1 = rows * cut * a.out.ksplit;
+  const int64_t blocks2 = (a.out.M + C2::BM - 1) / C2::BM * (cols - cut) * a.out.ksplit;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(blocks1 + blocks2)), dim3(C1::THREADS), (unsigned)lds, s,
+                     a, (int)cut, (int)cols, (uint32_t)blocks1);
   return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch_type(const Fp8Gemm &a, int tile, hipStream_t s) {
-  if (tile == 256) return launch_cfg<Fp8Cfg<T, 256, 256, 2, 4, 2>>(a, s);
+  using Wide = Fp8Cfg<T, 256, 256, 2, 4, 2>;
+  using Tail = Fp8Cfg<T, 128, 256, 2, 4, 2>;
+  using Small = Fp8Cfg<T, 128, 128, 2, 2, 2>;
+  using Deep = Fp8Cfg<T, 128, 128, 2, 2, 4>;
+  if (tile == 256) return launch_cfg<Wide, Tail>(a, s);
   const int64_t blocks = (a.out.M + 127) / 128 * ((a.out.N + 127) / 128) * a.out.ksplit;
-  return deep_ring(blocks) ? launch_cfg<Fp8Cfg<T, 128, 128, 2, 2, 4>>(a, s)
-                           : launch_cfg<Fp8Cfg<T, 128, 128, 2, 2, 2>>(a, s);
+  return deep_ring(blocks) ? launch_cfg<Deep, Deep>(a, s) : launch_cfg<Small, Small>(a, s);
 }
 
 }  // namespace fp8

@@ -251,6 +251,8 @@ __device__ __forceinline__ void run_tiles(int64_t lda, int64_t ldb, int nsegs, u
     cur = ld.out, left = nst;
     active = wm * C::WM < cur.rows && wn * C::WO < cur.cols;
   };
+  // whether the sums go to `part` in fp32
+  const bool wide = C::LA == Lay::RowK && kernel_args<K>()->a.to_parts;
   auto store_tile = [&]() {
     // computed here, not kept in registers beside the loop's
     int lane = threadIdx.x & 63;
@@ -288,6 +290,24 @@ __device__ __forceinline__ void run_tiles(int64_t lda, int64_t ldb, int nsegs, u
         __builtin_amdgcn_raw_buffer_store_b128(pack8<T>(gv), ry,
                                                in ? r * ldy * 2 + c0 * 2 : kOob, 0, 0);
       }
+    } else if (wide) {
+      const int ldp = (int)k->a.N;
+      float *const part = k->a.part + (int64_t)cur.row0 * ldp + cur.n0;
+      const rsrc_t rp = make_rsrc(part, ((int64_t)(cur.rows - 1) * ldp + cols) * 4);
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int q = 0; q < NI / 2; ++q) {
+          float v[8];
+          join_blocks(acc[mi * NI + 2 * q], acc[mi * NI + 2 * q + 1], v);
+          const int c = c0 + 32 * q, off = ((r0 + mi * 16) * ldp + c) * 4;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const u32x4 w = __builtin_bit_cast(
+                u32x4, f32x4{v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]});
+            __builtin_amdgcn_raw_buffer_store_b128(w, rp, c < cur.cols ? off + 16 * e : kOob, 0, 0);
+          }
+        }
     } else {
       // Two instructions a row block, of 8 rows and 128 bytes of each: lanes 8 apart swap
       // halves, so that whole lines are written.
@@ -352,6 +372,8 @@ __device__ __forceinline__ void run_tiles(int64_t lda, int64_t ldb, int nsegs, u
       wait_vm<0>();
     else if (C::GATED && saves)
       wait_vm<3 * STORES>();
+    else if (!C::GATED && wide)
+      wait_vm<2 * STORES>();
     else
       wait_vm<STORES>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");

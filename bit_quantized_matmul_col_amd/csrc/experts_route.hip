@@ -17,6 +17,8 @@
 //
 // What bounds it: for few rows the launch and the k dependent steps (about 0.2 us each); for
 // many the instructions of the selection, not the 4 bytes a logit.
+#include <type_traits>
+
 #include "experts.hpp"
 #include "llmint8.h"
 
@@ -56,6 +58,11 @@ __device__ inline F wave_add(F v) {
 __device__ inline uint64_t ordered(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 to 0
   return b >> 63 ? ~b : b | 1ull << 63;
+}
+
+__device__ inline uint32_t ordered(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.f);
+  return b >> 31 ? ~b : b | 1u << 31;
 }
 
 __device__ inline float load_logit(const void *p, int64_t i, int dtype) {
@@ -103,9 +110,14 @@ __device__ inline float mix(const Route &r, const float *x, float c) {
   return has ? expf(c - top) / sum : 0.f;
 }
 
-template <int V>
+// LOGITS: the logits themselves have the order, and 32-bit keys.
+template <int V, bool LOGITS>
 __global__ __launch_bounds__(64 * kRows) void k_route(Route r, int32_t *ids, float *weights) {
-  extern __shared__ double values[];
+  using Key = std::conditional_t<LOGITS, uint32_t, uint64_t>;
+  using Value = std::conditional_t<LOGITS, float, double>;
+  constexpr Value kNone = -__builtin_inf();
+  extern __shared__ double values_v[];
+  Value *const values = (Value *)values_v;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t row = (int64_t)blockIdx.x * kRows + wv;
   if (row >= r.M) return;  // no barrier below: a wave uses its own part of `values`
@@ -113,8 +125,8 @@ __global__ __launch_bounds__(64 * kRows) void k_route(Route r, int32_t *ids, flo
   load_row<V>(r, row, lane, x);
 
   // the values that experts are chosen by
-  double val[V];
-  if (!r.bias && r.group_best == 1) {
+  Value val[V];
+  if constexpr (LOGITS) {
 #pragma unroll
     for (int v = 0; v < V; ++v) val[v] = x[v];
   } else {
@@ -142,56 +154,67 @@ __global__ __launch_bounds__(64 * kRows) void k_route(Route r, int32_t *ids, flo
       if (r.bias && e < r.E) val[v] += (double)r.bias[e];
     }
   }
-  uint64_t key[V];
+  Key key[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    key[v] = x[v] > -kInf && val[v] > -(double)kInf ? ordered(val[v]) : 0;
+  for (int v = 0; v < V; ++v) key[v] = x[v] > -kInf && val[v] > kNone ? ordered(val[v]) : 0;
 
   if (r.groups > 1) {
-    // lane g takes group g: its value, then how many groups come before it
-    double *const mine = values + (size_t)wv * r.E;
+    // `per` lanes (a power of two) have a group: its best values, then how many groups come
+    // before it
+    Value *const mine = values + (size_t)wv * r.E;
     const int each = r.E / r.groups;
+    int per = 1;
+    while (2 * per * r.groups <= kWave) per *= 2;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (lane + 64 * v < r.E) mine[lane + 64 * v] = key[v] ? val[v] : -(double)kInf;
+      if (lane + 64 * v < r.E) mine[lane + 64 * v] = key[v] ? val[v] : kNone;
     __builtin_amdgcn_wave_barrier();
-    double best = -(double)kInf, second = best;
-    if (lane < r.groups)
-      for (int i = 0; i < each; ++i) {
-        const double d = mine[lane * each + i];
+    Value best = kNone, second = kNone;
+    const int group = lane / per;
+    if (group < r.groups)
+      for (int i = lane % per; i < each; i += per) {
+        const Value d = mine[group * each + i];
         second = d > best ? best : d > second ? d : second;
         best = d > best ? d : best;
       }
-    if (r.group_best == 2 && second > -(double)kInf) best += second;
+    for (int off = 1; off < per; off <<= 1) {
+      const Value b = __shfl_xor(best, off, kWave), s = __shfl_xor(second, off, kWave);
+      const Value low = b < best ? b : best, high = s > second ? s : second;
+      second = low > high ? low : high;
+      best = b > best ? b : best;
+    }
+    if (r.group_best == 2 && second > kNone) best += second;
     int before = 0;
     for (int g = 0; g < r.groups; ++g) {
-      const double o = __shfl(best, g, kWave);
-      before += o > best || (o == best && g < lane);
+      const Value o = __shfl(best, g * per, kWave);
+      before += o > best || (o == best && g < group);
     }
-    const uint64_t keep = __ballot(lane < r.groups && before < r.top_groups);
+    const uint64_t keep = __ballot(group < r.groups && before < r.top_groups);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int e = lane + 64 * v;
-      if (e < r.E && !(keep >> (e / each) & 1)) key[v] = 0;
+      if (e < r.E && !(keep >> (e / each * per) & 1)) key[v] = 0;
     }
   }
 
   int id = -1;        // of slot `lane`
   float c = -kInf;    // its logit
   for (int j = 0; j < r.k; ++j) {
-    uint64_t best = key[0];
+    Key best = key[0];
     int bv = 0;
     float bx = x[0];
 #pragma unroll
     for (int v = 1; v < V; ++v)
       if (key[v] > best) best = key[v], bv = v, bx = x[v];  // the lower index of equals
-    const uint32_t hi = (uint32_t)(best >> 32), lo = (uint32_t)best;
+    const uint32_t hi = (uint32_t)(LOGITS ? best : best >> (LOGITS ? 0 : 32)), lo = (uint32_t)best;
     const uint32_t top = wave_umax(hi);
     if (top == 0) break;  // every number's upper word is positive: none is left
     uint64_t who = __ballot(hi == top);
     if (who & (who - 1)) {
-      const uint32_t low = wave_umax(hi == top ? lo : 0);
-      who = __ballot(hi == top && lo == low);
+      if constexpr (!LOGITS) {
+        const uint32_t low = wave_umax(hi == top ? lo : 0);
+        who = __ballot(hi == top && lo == low);
+      }
       if (who & (who - 1)) {
         const bool in = who >> lane & 1;
         const uint32_t first = wave_umax(in ? ~(uint32_t)(lane + 64 * bv) : 0);
@@ -375,10 +398,13 @@ hipError_t with_width(int E, F f) {
 }  // namespace
 
 hipError_t launch_route(const Route &r, int32_t *ids, float *weights, hipStream_t s) {
-  const size_t lds = r.groups > 1 ? (size_t)kRows * r.E * sizeof(double) : 0;
+  const bool logits = !r.bias && r.group_best == 1;
+  const size_t value = logits ? sizeof(float) : sizeof(double);
+  const size_t lds = r.groups > 1 ? (size_t)kRows * r.E * value : 0;
   return with_width(r.E, [&](auto w) {
-    hipLaunchKernelGGL((k_route<decltype(w)::value>), dim3((unsigned)((r.M + kRows - 1) / kRows)),
-                       dim3(64 * kRows), lds, s, r, ids, weights);
+    auto *kern = logits ? k_route<decltype(w)::value, true> : k_route<decltype(w)::value, false>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)((r.M + kRows - 1) / kRows)), dim3(64 * kRows), lds, s,
+                       r, ids, weights);
     return hipGetLastError();
   });
 }

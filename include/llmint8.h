@@ -490,8 +490,7 @@ int llmint8_experts_gated(const uint16_t *X, int64_t M, int64_t K, int64_t ldx,
 /*
  * Gradients of llmint8_experts_gated: with d = w[pair] dH[r],
  *   dG = d * U * act'(G) and dU = d * act(G) (rounded to 16 bits, the products' operands),
- *   dX[i] = the sum over token i's rows of dG . Wg_e^T + dU . Wu_e^T (each row's rounded to 16
- *           bits before the sum, which is fp32),
+ *   dX[i] = the sum over token i's rows of dG . Wg_e^T + dU . Wu_e^T (fp32, rounded once),
  *   dWg_e = X_e^T . dG_e, dWu_e = X_e^T . dU_e over expert e's rows (zeros without any),
  *   dweights[pair] = sum over n of dH[r] act(G[r]) U[r] (fp32; 0 without a row).
  * dX, dweights and the pair dWg, dWu (leading dimension lddw, stride_dw elements from expert to

@@ -229,7 +229,7 @@ def gated_backward(dH, X, Wg, Wu, G, U, p, w, name, dtype):
         x2, e2 = fo.rounded_product(du, Wu[e].t(), eu, True, dtype)
         row = x1 + x2
         dX[0].index_add_(0, token, row)
-        dX[1].index_add_(0, token, fo.stored(row, 2 * (e1 + e2), dtype))
+        dX[1].index_add_(0, token, 2 * (e1 + e2))
         size.index_add_(0, token, row.abs())
         for (v, dv), to in ((fo.rounded_product(X[token].t(), dg, eg, False, dtype), dWg),
                             (fo.rounded_product(X[token].t(), du, eu, False, dtype), dWu)):

@@ -89,7 +89,8 @@ def test_route_backward_of_an_expert_named_twice_and_of_none(lm):
 
 
 @pytest.mark.parametrize("M,k,E", [(1, 1, 1), (1, 8, 64), (5, 3, 7), (333, 3, 11), (1000, 8, 256),
-                                   (4097, 2, 3), (700, 64, 1024), (8192, 1, 4)])
+                                   (4097, 2, 3), (700, 64, 1024), (8192, 1, 4), (9000, 8, 40),
+                                   (70001, 2, 5)])
 def test_plan(lm, M, k, E):
     say("plan", M, k, E)
     g = gen(M + k + E)
