@@ -1000,6 +1000,8 @@ def llmint8_expert_plan(ids: torch.Tensor, experts: int) -> ExpertPlan:
     _need(ids, "ids", torch.int32, 2)
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
+    if not 1 <= experts <= 1024:
+        raise ValueError(f"experts must be from 1 to 1024, got {experts}")
     M, k = ids.shape
     # one allocation: the parts begin at multiples of 16 bytes
     a, b = (experts + 4) // 4 * 4, (M * k + 3) // 4 * 4

@@ -10,6 +10,10 @@ namespace llmint8 {
 constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxTopk = 64;
 constexpr int64_t kMaxGroups = 64;
+// Rows of an expert, on the mean, up to which the few-row kernel is considered.
+constexpr int64_t kFewRows = 200;
+// Pairs of a token and an expert: passes with a wave for each have fewer than 2^32 threads.
+constexpr int64_t kMaxPairs = (int64_t)1 << 25;
 
 struct Route {
   const void *logits;  // [M x ld], dtype 0 fp16, 1 bf16, 2 fp32
@@ -43,8 +47,8 @@ FfnPlan experts_plan(FfnKind kind, int64_t pairs, int E, int64_t N, int64_t K);
 
 // Products over the rows of each expert: `a` for all rows (a.M = the number of pairs, a.b and
 // a.pairs those of expert 0 and row 0); expert e's B is bstride elements after the last's.
-// Forward: rows as they are, sums to a.part in fp32 or to a.y. Gated: rows of the tokens.
-// GradX: rows as they are.
+// Forward and GradX: rows as they are, sums to a.y, or to a.part in fp32. Gated: rows of the
+// tokens, or as they are.
 hipError_t launch_expert_rows(FfnKind kind, int dtype, const FfnGemm &a, const Pairs &p,
                               int64_t bstride, const FfnPlan &plan, hipStream_t s);
 hipError_t launch_expert_skinny(int dtype, bool gated, const FfnGemm &a, const Pairs &p,

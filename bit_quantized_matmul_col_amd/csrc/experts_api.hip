@@ -22,22 +22,6 @@ hipError_t launch_expert_rows(FfnKind kind, int dtype, const FfnGemm &a, const P
   return launch_expert_grad_x(dtype, a, p, bstride, plan.tile, s);
 }
 
-FfnPlan experts_plan(FfnKind kind, int64_t pairs, int E, int64_t N, int64_t K) {
-  const int64_t used = E < pairs ? E : pairs, each = pairs / used;
-  const bool forward = kind != FfnKind::GradX;
-  if (forward && each <= 64) {
-    const int rows = each <= 12 ? 16 : each <= 28 ? 32 : 64;
-    const int64_t groups = (pairs + rows - 1) / rows > used ? (pairs + rows - 1) / rows : used;
-    int cols = 64;
-    if (!(kind == FfnKind::Gated && rows == 64) && groups * N / 128 >= 512) cols = 128;
-    int parts = 1;
-    const int64_t blocks = groups * ((N + cols - 1) / cols);
-    while (parts < 8 && blocks * parts * 2 <= 256 && K / (64 * 4 * parts * 2) >= 2) parts *= 2;
-    return FfnPlan{true, cols, parts, rows};
-  }
-  return FfnPlan{false, each >= 160 ? 256 : 128, 1, 0};
-}
-
 }  // namespace llmint8
 
 namespace {
@@ -49,11 +33,15 @@ void check_rows(Check &c, int64_t M, int64_t K, int64_t N, int64_t E, int64_t k)
   c.dims(M, K, N);
   c.need(E > 0 && k > 0);
   c.need(E <= kMaxExperts && k <= kMaxTopk && k <= E);
-  c.need(M > 0 && k > 0 && M < kMaxDim && M * k < kMaxDim);
+  c.need(k > 0 && M <= (kMaxPairs - 1) / k);
   if (c.arg) return;
-  // blocks of the largest launch: tiles of 16 rows by 32 columns in 8 parts, and the tiles of dW
-  const int64_t rows = M * k, wide = (K > N ? K : N) / 32 + 1;
-  c.want((rows / 16 + E) * wide < kMaxDim && E * (K / 128 + 1) * (N / 128 + 1) < kMaxDim);
+  // Tiles are counted in 32 bits. Few-row blocks (16 by 64 columns; in parts only where they are
+  // few) have fewer than 2^32 threads.
+  const int64_t rows = M * k, wide = K > N ? K : N, most = (kFewRows + 1) * E;
+  const int64_t few = rows < most ? rows : most;
+  c.want((rows / 128 + E) * (wide / 128 + 1) < kMaxDim);
+  c.want(E * (K / 128 + 1) * (N / 128 + 1) < kMaxDim);
+  c.want((few / 16 + E) * (wide / 64 + 1) < (int64_t)1 << 24);
 }
 
 bool rows_ok(int64_t M, int64_t K, int64_t N, int64_t E, int64_t k) {
@@ -153,7 +141,7 @@ bool route_ok(Check &c, const void *logits, int64_t M, int64_t E, int64_t ld, in
     o = *opts;
   }
   c.need(M > 0 && E > 0 && k > 0 && E <= kMaxExperts && k <= E && k <= kMaxTopk);
-  c.need(M < kMaxDim && (k <= 0 || M * k < kMaxDim));
+  c.need(k > 0 && M <= (kMaxPairs - 1) / k);
   c.need(logits && ld >= E && ld < kMaxLd);
   c.need(dtype == LLMINT8_FP16 || dtype == LLMINT8_BF16 || dtype == LLMINT8_FP32);
   c.need(o.scores == LLMINT8_SCORE_SOFTMAX || o.scores == LLMINT8_SCORE_SIGMOID);
@@ -309,7 +297,7 @@ LLMINT8_EXPORT int llmint8_experts_gated_backward(
     FfnGemm a = rows_gemm(dg, N, Wg, ldw, K, N, p, nullptr, 0);
     a.a[1] = du, a.b[1] = Wu, a.segs = 2;
     a.part = xrows, a.to_parts = 1;
-    const FfnPlan plan = experts_plan(FfnKind::GradX, p.rows(), p.E, K, N);
+    const FfnPlan plan = experts_plan(FfnKind::GradX, p.rows(), p.E, K, 2 * N);
     e = launch_expert_rows(FfnKind::GradX, dtype, a, p, stride_w, plan, s);
     if (e == hipSuccess)
       e = launch_combine(dtype, Combine{nullptr, xrows, 1, K, nullptr, 0, dX, lddx}, p, s);

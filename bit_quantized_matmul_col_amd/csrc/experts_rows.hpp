@@ -20,7 +20,10 @@ __global__ __launch_bounds__(C::THREADS, 2) void k_expert_rows(ExpertRowsArgs ar
   ExpertTable table((uint8_t *)smem_v + tiles_lds<C>(), args.E);
   table.fill<C::BM>(args.offsets, args.a.all_rows);
   __syncthreads();
-  const uint32_t tiles = table.tiles() * (uint32_t)args.cols;
+  // (offsets that no plan writes would count rows twice)
+  const uint32_t most = (uint32_t)(args.a.all_rows / C::BM + args.E);
+  const uint32_t found = table.tiles();
+  const uint32_t tiles = (found < most ? found : most) * (uint32_t)args.cols;
   // The tiles of an expert in consecutive places, its tile rows in groups of 8, a group column
   // by column, as in tile_at: neighbours share weights and rows, and the weights, which
   // are most of what is read, leave HBM once.

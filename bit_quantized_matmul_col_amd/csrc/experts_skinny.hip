@@ -1,6 +1,6 @@
 // The experts' forward products where an expert has few rows (single tokens, decoding
-// batches): blocks of ffn_skinny.hpp, a group of up to 16, 32 or 64 rows of one expert by 32,
-// 64 or 128 columns, which read that expert's weights once. The weights of the experts that
+// batches): blocks of ffn_skinny.hpp, a group of up to 16, 32 or 64 rows of one expert by 64
+// or 128 columns, which read that expert's weights once. The weights of the experts that
 // were chosen bound it.
 #include "experts_tile.hpp"
 #include "ffn_skinny.hpp"
@@ -45,8 +45,6 @@ hipError_t launch_few_cols(const FfnGemm &a, const Pairs &p, int64_t bstride, in
                            hipStream_t s) {
   if constexpr (!(GATED && MT == 4))
     if (cols == 128) return launch_few_cfg<SkinnyCfg<T, GATED, MT, 128, true>>(a, p, bstride, s);
-  if constexpr (MT != 4)
-    if (cols == 32) return launch_few_cfg<SkinnyCfg<T, GATED, MT, 32, true>>(a, p, bstride, s);
   return launch_few_cfg<SkinnyCfg<T, GATED, MT, 64, true>>(a, p, bstride, s);
 }
 

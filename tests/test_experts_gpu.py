@@ -132,6 +132,12 @@ def ids_of(g, M, E, k, masked):
     return ids
 
 
+def rounded(lm, M, K, N, E, k):
+    """Whether the second product's rows go through 16 bits before they are summed (with few rows
+    an expert they stay in fp32, and the workspace is of that size, in multiples of 256 bytes)."""
+    return lm.llmint8_experts_matmul_workspace_size(M, K, N, E, k) <= -(-M * k * K * 2 // 256) * 256
+
+
 class Experts:
     def __init__(self, lm, M, K, N, E, k, masked, dtype, seed=0):
         g = gen(M + 3 * K + 5 * N + E + seed)
@@ -148,8 +154,7 @@ class Experts:
         self.G, self.U = rand(g, R, N, dtype, 1.5), rand(g, R, N, dtype, 1.5)
         self.R, self.dY = rand(g, M, K, dtype), rand(g, M, K, dtype, 0.5)
         self.name = fo.ACTS[1 + (M + K + N) // 8 % 4]
-        # few rows an expert: the second product's sums stay in fp32 until the end
-        self.rounded = R // min(E, R) > 64
+        self.rounded = rounded(lm, M, K, N, E, k)
 
 
 def rows_only(got, want, last):
