@@ -142,7 +142,9 @@ def lib() -> C.CDLL:
             query.argtypes, query.restype = [i64, i64, i64], sz
         L.llmint8_route.argtypes = [p, i64, i64, i64, i, i64, p, p, p, p]
         L.llmint8_route_backward.argtypes = [p, p, i64, i64, i64, i, i64, p, p, p, i64, p]
-        L.llmint8_expert_plan.argtypes = [p, i64, i64, i64, p, p, p, p]
+        L.llmint8_expert_plan.argtypes = [p, i64, i64, i64, p, p, p, p, sz, p]
+        L.llmint8_expert_plan_workspace_size.argtypes = [i64, i64, i64]
+        L.llmint8_expert_plan_workspace_size.restype = sz
         L.llmint8_experts_gated.argtypes = [p, i64, i64, i64, p, p, i64, i64, i64, p, p, i, i, p,
                                             i64, p, p, i64, p, sz, p]
         L.llmint8_experts_gated_backward.argtypes = [p, i64, i64, i64, p, i64, i64, p, p, i64, i64,
@@ -1003,14 +1005,16 @@ def llmint8_expert_plan(ids: torch.Tensor, experts: int) -> ExpertPlan:
     if not 1 <= experts <= 1024:
         raise ValueError(f"experts must be from 1 to 1024, got {experts}")
     M, k = ids.shape
-    # one allocation: the parts begin at multiples of 16 bytes
-    a, b = (experts + 4) // 4 * 4, (M * k + 3) // 4 * 4
-    held = torch.empty((a + 2 * b,), dtype=torch.int32, device=ids.device)
-    plan = ExpertPlan(held[:experts + 1], held[a:a + M * k],
-                      held[a + b:a + b + M * k].view(M, k))
+    need = lib().llmint8_expert_plan_workspace_size(M, k, experts)
+    # one allocation: the parts, the workspace first, begin at multiples of 16 bytes
+    w, a, b = (need + 15) // 16 * 4, (experts + 4) // 4 * 4, (M * k + 3) // 4 * 4
+    held = torch.empty((w + a + 2 * b,), dtype=torch.int32, device=ids.device)
+    plan = ExpertPlan(held.as_strided((experts + 1,), (1,), w),
+                      held.as_strided((M * k,), (1,), w + a),
+                      held.as_strided((M, k), (k, 1), w + a + b))
     at = held.data_ptr()
-    _launch(lib().llmint8_expert_plan, ids, ids.data_ptr(), M, k, experts, at, at + 4 * a,
-            at + 4 * (a + b))
+    _launch(lib().llmint8_expert_plan, ids, ids.data_ptr(), M, k, experts, at + 4 * w,
+            at + 4 * (w + a), at + 4 * (w + a + b), at if need else None, need)
     return plan
 
 

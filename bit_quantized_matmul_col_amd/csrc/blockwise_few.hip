@@ -80,7 +80,8 @@ __global__ __launch_bounds__(C::THREADS, 1) void k_fp8_few(Fp8Gemm a) {
         const int r = 16 * m + i, off = r * K + k;
         st.x[2 * m] = load16(rx, in0 ? off : kOob);
         st.x[2 * m + 1] = load16(rx, in1 ? off + 64 : kOob);
-        st.sx[m] = __builtin_amdgcn_raw_buffer_load_b8(rsx, b < nb ? r * (int)a.x.lds + b : kOob, 0, 0);
+        const int at = b < nb ? r * (int)a.x.lds + b : kOob;
+        st.sx[m] = __builtin_amdgcn_raw_buffer_load_b8(rsx, at, 0, 0);
       }
     }
     st.sw = __builtin_amdgcn_raw_buffer_load_b8(rsw, b < nb ? b : kOob, 0, 0);
@@ -173,7 +174,8 @@ hipError_t launch_few_cfg(const Fp8Gemm &a, hipStream_t s) {
   hipError_t e = hipFuncSetAttribute((const void *)kern,
                                      hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
   if (e != hipSuccess) return e;
-  const int64_t blocks = (a.out.N + C::CB - 1) / C::CB * ((a.out.M + 16 * C::MT - 1) / (16 * C::MT));
+  const int64_t groups = (a.out.M + 16 * C::MT - 1) / (16 * C::MT);
+  const int64_t blocks = (a.out.N + C::CB - 1) / C::CB * groups;
   hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(C::THREADS), C::LDS, s, a);
   return hipGetLastError();
 }

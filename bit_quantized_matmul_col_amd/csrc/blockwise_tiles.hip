@@ -13,6 +13,11 @@
 // twice the reduction. So A's fragments go through a ring of four registers sets, read
 // two steps ahead, and B's (all columns of the wave) are replaced one by one by the next
 // stage's behind their last use.
+//
+// What bounds it: power. 8192 x 8192 x 28672 runs at 2.3 PFLOP/s, 1.69 ms, at a clock of 1.87 GHz
+// with the MFMAs busy for 0.55 of the time; a pass that codes X before it takes 44 us of that.
+// 1777 x 5120 x 13824 takes 119 us at 2.12 GHz and 8 us of coding: 378 tiles on 256 CUs, the last
+// 122 of them in halves (the call 144 us, with whole tiles 155).
 #include "blockwise_math.hpp"
 
 namespace llmint8 {
@@ -177,8 +182,10 @@ __device__ __forceinline__ void fp8_tile(const Fp8Gemm &a, uint32_t bid, int col
           // the scales of the next stage, behind their last use
           if (ni == 1 && mi >= MI - 2)
 #pragma unroll
-            for (int q = 0; q < (MI - 2) / 2; ++q) read_sx(next, s + 1, (mi - MI + 2) * (MI - 2) / 2 + q);
-          if (mi == MI - 1 && ni == NI - 1) read_sx(next, s + 1, MI - 2), read_sx(next, s + 1, MI - 1);
+            for (int q = 0; q < (MI - 2) / 2; ++q)
+              read_sx(next, s + 1, (mi - MI + 2) * (MI - 2) / 2 + q);
+          if (mi == MI - 1 && ni == NI - 1)
+            read_sx(next, s + 1, MI - 2), read_sx(next, s + 1, MI - 1);
           if (i % 2 == 1 && i / 2 < LPS - H) load(l, last, H + i / 2);
           const int r = i - (MI - 2) * NI;  // MFMAs since the waves met
           if (r >= 0) {

@@ -38,8 +38,10 @@ struct Pairs {
   __host__ __device__ int64_t rows() const { return tokens * k; }
 };
 
+// Bytes of its scratch: 0 for few pairs.
+size_t expert_plan_scratch(int64_t pairs, int E);
 hipError_t launch_expert_plan(const int32_t *ids, int64_t pairs, int E, int32_t *offsets,
-                              int32_t *order, int32_t *places, hipStream_t s);
+                              int32_t *order, int32_t *places, int32_t *scratch, hipStream_t s);
 
 // How a product over the experts' rows runs: square tiles of 256 or 128 rows, or the
 // few-row kernel with `tile` columns by `rows` rows; in how many parts the reduction is split.

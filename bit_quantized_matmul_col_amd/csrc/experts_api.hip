@@ -183,16 +183,22 @@ LLMINT8_EXPORT int llmint8_route_backward(const float *dweights, const void *log
   return hip_status(launch_route_backward(r, ids, dweights, dlogits, ldd, (hipStream_t)stream));
 }
 
+LLMINT8_EXPORT size_t llmint8_expert_plan_workspace_size(int64_t M, int64_t k, int64_t E) {
+  return rows_ok(M, 8, 8, E, k) ? expert_plan_scratch(M * k, (int)E) : 0;
+}
+
 LLMINT8_EXPORT int llmint8_expert_plan(const int32_t *ids, int64_t M, int64_t k, int64_t E,
                                        int32_t *offsets, int32_t *order, int32_t *places,
-                                       void *stream) {
+                                       void *workspace, size_t workspace_bytes, void *stream) {
   Check c;
   check_rows(c, M, 8, 8, E, k);
   c.need(ids && offsets && order && places);
   c.want(aligned16(ids) && aligned4(offsets) && aligned4(order) && aligned4(places));
   if (const int st = c.status()) return st;
-  return hip_status(
-      launch_expert_plan(ids, M * k, (int)E, offsets, order, places, (hipStream_t)stream));
+  const size_t need = expert_plan_scratch(M * k, (int)E);
+  if (const int st = check_workspace(workspace, workspace_bytes, need)) return st;
+  return hip_status(launch_expert_plan(ids, M * k, (int)E, offsets, order, places,
+                                       (int32_t *)workspace, (hipStream_t)stream));
 }
 
 LLMINT8_EXPORT size_t llmint8_experts_gated_workspace_size(int64_t M, int64_t K, int64_t N,

@@ -24,9 +24,10 @@ __global__ __launch_bounds__(kThreads) void k_take_rows(const uint16_t *x, int64
   });
 }
 
-// The rows of a token's pairs are summed in fp32, in the order of its choices. After tiles they
-// come in 16 bits: each was rounded once, as the sum will be. In fp32 they would take twice the
-// bytes of the largest pass next to the products (see launch_combined in experts_api.hip).
+// The rows of a token's pairs are summed in fp32, in the order of its choices. The second product's
+// tiles leave them in 16 bits: each was rounded once, as the sum will be, and fp32 would be twice
+// the bytes of the largest pass next to the product. dX's come in fp32, since they were summed from
+// operands that had been rounded already.
 template <class T, bool F32>
 __global__ __launch_bounds__(kThreads) void k_combine(Combine c, Pairs p, int cx_log2) {
   const int64_t rows = p.rows();

@@ -1,20 +1,20 @@
 // Which kernel a product over the experts' rows takes.
 //
-// The candidates are square tiles of 256 or 128 rows of an expert, and for the forward products the
-// few-row kernel with 16, 32 or 64 rows by 64 or 128 columns a block, whole or with the reduction in
-// 2 or 4 parts. The plan is the one with the smallest estimated time. How many rows each
-// expert has is known on the GPU alone, so the estimates take the mean and add a part of
-// a group for what each expert's last one lacks. Their constants were fitted to 3160 timed calls on
+// The candidates are square tiles of 256 or 128 rows of an expert, and for the forward products
+// the few-row kernel with 16, 32 or 64 rows by 64 or 128 columns a block, whole or with the
+// reduction in 2 or 4 parts. The plan is the one with the smallest estimated time. How many rows
+// each expert has is known on the GPU alone, so the estimates take the mean and add a part of a
+// group for what each expert's last one lacks. Their constants were fitted to 3160 timed calls on
 // MI355X (bf16, graph replay; 8 to 128 experts, 512 x 512 to 4096 x 11008, 1 to 400 rows an
-// expert, unevenly spread): the plans chosen by them cost 3.7 % more than the best
-// candidate (geometric mean over 224 products, at worst 48 %, where the spread makes one more round of
+// expert, unevenly spread): the plans chosen by them cost 3.7 % more than the best candidate
+// (geometric mean over 224 products, at worst 48 %, where the spread makes one more round of
 // 256-tiles than the mean does). Some of the choices, in microseconds:
-//   2 of 16 experts, 1 token, 4096 x 2048, gated    16 rows by 64 columns in 4 parts 20, whole 27
-//   8 of 128, 8 tokens, 768 x 2048, second product  16 rows by 64 columns 25.4, by 128 26.1
-//   8 of 128, 192 tokens, the same                  128-tiles 39, few rows 50
-//   2 of 8, 160 tokens, 11008 x 4096, the same      64 rows by 128 columns in 2 parts 153, whole 170
-//   4 of 32, 720 tokens, 2048 x 1024, gated         256-tiles 63, 128-tiles 75, few rows 84
-//   8 of 32, 1600 tokens, 7168 x 2048, gated        256-tiles 872, 128-tiles 985
+//   2 of 16, 1 token, 4096 x 2048, gated             16 rows by 64 columns in 4 parts 20, whole 22
+//   8 of 128, 8 tokens, 768 x 2048, second product   16 rows by 64 columns 25.4, by 128 26.1
+//   8 of 128, 192 tokens, the same                   128-tiles 39, few rows 50
+//   2 of 8, 160 tokens, 11008 x 4096, the same       64 rows by 128 in 2 parts 153, whole 180
+//   4 of 32, 720 tokens, 2048 x 1024, gated          256-tiles 63, 128-tiles 75, few rows 84
+//   8 of 32, 1600 tokens, 7168 x 2048, gated         256-tiles 872, 128-tiles 985
 // The plan is a function of the shape alone, so that the workspace query and the call agree.
 #include "experts.hpp"
 

@@ -315,8 +315,8 @@ __global__ __launch_bounds__(64 * kRows) void k_route_backward(Route r, const in
 // before e, which is where e's rows begin, and e's own in each wave's stretch of the pairs,
 // then goes through them once more and puts each at its place. So one launch does it, pairs
 // of an expert keep their order and no atomic decides anything; block E has the pairs without an
-// expert. Every block reads all ids twice, from L2: 65536 pairs of 256 experts are 131 MB of
-// such reads, 0.5 MB a CU.
+// expert. Every block reads all ids twice, from L2, at what one CU takes in.
+constexpr int64_t kPlanOnce = 24576;  // pairs up to which this one launch is quicker
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
 
 __global__ __launch_bounds__(kPlanThreads) void k_expert_plan(const int32_t *ids, int64_t pairs,
@@ -382,6 +382,128 @@ __global__ __launch_bounds__(kPlanThreads) void k_expert_plan(const int32_t *ids
   }
 }
 
+// More pairs: in chunks, so that a CU reads its own part of the ids alone. First each chunk's
+// pairs of every expert are counted; then a chunk's block adds up what the chunks before it have,
+// which is where its pairs of each expert go, and puts them there in their order: lanes with
+// the same expert find each other by a ballot for each bit of its number. A CU keeps about 256
+// lines in flight, 37 KB a microsecond, which is what bounds the one launch above: 131072 pairs
+// of 256 experts 26.5 us, in chunks 11.7; 65536 pairs 14.9 and 9.6; 16384 pairs 6.1 and 7.5.
+constexpr int kChunkThreads = 1024, kChunkWaves = kChunkThreads / 64;
+
+// The expert of pair p of a chunk that ends at p1; E: none; -1: no pair.
+__device__ inline int pair_expert(const int32_t *ids, int64_t p, int64_t p1, int E) {
+  if (p >= p1) return -1;
+  const int id = ids[p];
+  return (uint32_t)id < (uint32_t)E ? id : E;
+}
+
+__global__ __launch_bounds__(kChunkThreads) void k_plan_count(const int32_t *ids, int64_t pairs,
+                                                             int E, int64_t chunk,
+                                                             int32_t *counts) {
+  extern __shared__ int32_t hist[];  // [E + 1]
+  for (int e = threadIdx.x; e <= E; e += kChunkThreads) hist[e] = 0;
+  __syncthreads();
+  const int64_t p0 = blockIdx.x * chunk, p1 = p0 + chunk < pairs ? p0 + chunk : pairs;
+  for (int64_t p = p0 + threadIdx.x; p < p1; p += kChunkThreads)
+    atomicAdd(hist + pair_expert(ids, p, p1, E), 1);  // sums of ones: in any order the same
+  __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += kChunkThreads)
+    counts[(int64_t)blockIdx.x * (E + 1) + e] = hist[e];
+}
+
+__global__ __launch_bounds__(kChunkThreads) void k_plan_place(const int32_t *ids, int64_t pairs,
+                                                             int E, int64_t chunk,
+                                                             const int32_t *counts,
+                                                             int32_t *offsets, int32_t *order,
+                                                             int32_t *places) {
+  extern __shared__ int32_t smem[];
+  const int n = E + 1;
+  int32_t *const base = smem, *const mine = smem + n;  // [n], [waves][n]
+  __shared__ int sums[kChunkWaves];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int chunks = gridDim.x, me = blockIdx.x;
+  // the chunks before this one and all of them, several threads an expert
+  for (int e = t; e < n; e += kChunkThreads) base[e] = 0, mine[e] = 0;
+  __syncthreads();
+  const int parts = n < kChunkThreads ? kChunkThreads / n : 1;
+  for (int i = t; i < n * parts; i += kChunkThreads) {
+    const int e = i % n;
+    int prior = 0, all = 0;
+#pragma unroll 16
+    for (int c = i / n; c < chunks; c += parts) {
+      const int v = counts[(int64_t)c * n + e];
+      prior += c < me ? v : 0, all += v;
+    }
+    atomicAdd(base + e, prior), atomicAdd(mine + e, all);
+  }
+  __syncthreads();
+  constexpr int PER = (int)(kMaxExperts + 1 + kChunkThreads - 1) / kChunkThreads;
+  const int per = (n + kChunkThreads - 1) / kChunkThreads;
+  int all[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = t * per + i;
+    all[i] = i < per && e < n ? mine[e] : 0;
+    sum += all[i];
+  }
+  int upto = sum;  // of the threads up to this one
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int o = __shfl_up(upto, off, kWave);
+    upto += lane >= off ? o : 0;
+  }
+  if (lane == 63) sums[wv] = upto;
+  __syncthreads();
+  int first = upto - sum;
+  for (int i = 0; i < wv; ++i) first += sums[i];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = t * per + i;
+    if (i >= per || e >= n) break;
+    base[e] += first;
+    if (me == 0) offsets[e] = first;
+    first += all[i];
+  }
+  __syncthreads();
+
+  const int64_t p0 = me * chunk, p1 = p0 + chunk < pairs ? p0 + chunk : pairs;
+  const int bits = 32 - __builtin_clz(n);
+  int32_t *const own = mine + wv * n;
+  for (int64_t s0 = p0; s0 < p1; s0 += kChunkThreads) {
+    for (int i = t; i < kChunkWaves * n; i += kChunkThreads) mine[i] = 0;
+    __syncthreads();
+    const int64_t p = s0 + t;
+    const int id = pair_expert(ids, p, p1, E);
+    uint64_t same = __ballot(id >= 0);  // the lanes with the same expert
+    for (int b = 0; b < bits; ++b) {
+      const bool bit = id >> b & 1;
+      const uint64_t m = __ballot(bit);
+      same &= bit ? m : ~m;
+    }
+    const int rank = __popcll(same & (((uint64_t)1 << lane) - 1));
+    if (id >= 0 && same >> lane == 1) own[id] = rank + 1;  // the last of them
+    __syncthreads();
+    if (id >= 0) {
+      int r = base[id] + rank;
+      for (int w = 0; w < wv; ++w) r += mine[w * n + id];
+      places[p] = id < E ? r : -1;
+      order[r] = id < E ? (int32_t)p : -1;
+    }
+    if (s0 + kChunkThreads >= p1) return;
+    __syncthreads();
+    for (int e = t; e < n; e += kChunkThreads)
+      for (int w = 0; w < kChunkWaves; ++w) base[e] += mine[w * n + e];
+    __syncthreads();
+  }
+}
+
+// At most 256 chunks, of whole blocks' threads.
+int64_t plan_chunk(int64_t pairs) {
+  const int64_t subs = (pairs + kChunkThreads - 1) / kChunkThreads;
+  return (subs + 255) / 256 * kChunkThreads;
+}
+
 template <int V>
 struct Width {
   static constexpr int value = V;  // logits a lane
@@ -419,10 +541,30 @@ hipError_t launch_route_backward(const Route &r, const int32_t *ids, const float
   });
 }
 
+size_t expert_plan_scratch(int64_t pairs, int E) {
+  if (pairs <= kPlanOnce) return 0;
+  const int64_t chunk = plan_chunk(pairs);
+  return (size_t)((pairs + chunk - 1) / chunk * (E + 1)) * sizeof(int32_t);
+}
+
 hipError_t launch_expert_plan(const int32_t *ids, int64_t pairs, int E, int32_t *offsets,
-                              int32_t *order, int32_t *places, hipStream_t s) {
-  hipLaunchKernelGGL(k_expert_plan, dim3((unsigned)(E + 1)), dim3(kPlanThreads), 0, s, ids, pairs,
-                     E, offsets, order, places);
+                              int32_t *order, int32_t *places, int32_t *scratch, hipStream_t s) {
+  if (pairs <= kPlanOnce) {
+    hipLaunchKernelGGL(k_expert_plan, dim3((unsigned)(E + 1)), dim3(kPlanThreads), 0, s, ids,
+                       pairs, E, offsets, order, places);
+    return hipGetLastError();
+  }
+  const int64_t chunk = plan_chunk(pairs);
+  const dim3 grid((unsigned)((pairs + chunk - 1) / chunk));
+  const unsigned row = (unsigned)(E + 1) * sizeof(int32_t);
+  hipLaunchKernelGGL(k_plan_count, grid, dim3(kChunkThreads), row, s, ids, pairs, E, chunk,
+                     scratch);
+  const unsigned lds = (1 + kChunkWaves) * row;
+  const hipError_t e = hipFuncSetAttribute((const void *)k_plan_place,
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_plan_place, grid, dim3(kChunkThreads), lds, s, ids, pairs, E, chunk, scratch,
+                     offsets, order, places);
   return hipGetLastError();
 }
 

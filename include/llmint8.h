@@ -457,7 +457,8 @@ int llmint8_route_backward(const float *dweights, const void *logits, int64_t M,
  *   order    [M k]: the pair of each row, an expert's pairs in rising order; -1 behind the last.
  *   places   [M x k]: the row of each pair, -1 for an id outside 0 .. E - 1, which has none.
  * llmint8_expert_plan fills the three from ids [M x k]; nothing depends on the order in which
- * blocks run. The calls below take them in an llmint8_expert_rows, and check what they read from
+ * blocks run. Its workspace has llmint8_expert_plan_workspace_size bytes (may be 0: NULL then).
+ * The calls below take them in an llmint8_expert_rows, and check what they read from
  * them against the buffers' sizes; a plan of other ids gives other results but stays within.
  */
 typedef struct llmint8_expert_rows {
@@ -466,8 +467,10 @@ typedef struct llmint8_expert_rows {
   const int32_t *places;
   int64_t E, k;
 } llmint8_expert_rows;
+size_t llmint8_expert_plan_workspace_size(int64_t M, int64_t k, int64_t E);
 int llmint8_expert_plan(const int32_t *ids, int64_t M, int64_t k, int64_t E, int32_t *offsets,
-                        int32_t *order, int32_t *places, void *stream);
+                        int32_t *order, int32_t *places, void *workspace, size_t workspace_bytes,
+                        void *stream);
 
 /*
  * The experts' gated blocks: for the row r of the pair of token i and expert e

@@ -36,6 +36,30 @@ def test_experts_variants(lm, M, K, N, E, k, masked, dtype):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("M,k,E", [(24576, 1, 3), (24577, 1, 3), (4100, 8, 1024), (12099, 3, 257),
+                                   (40000, 8, 1024), (300001, 1, 7), (262144, 1, 1),
+                                   (131073, 64, 65)])
+def test_plans_of_many_pairs(lm, M, k, E):
+    """One launch, and chunks of 1024 pairs and of more, against a stable sort by expert."""
+    say("plan", M, k, E)
+    g = gen(M)
+    ids = torch.randint(-2, E + 2, (M, k), generator=g, device="cuda", dtype=torch.int32)
+    ids[M // 3:M // 2] = E // 2  # long runs of one expert
+    key = torch.where((ids < 0) | (ids >= E), E, ids).reshape(-1).cpu().long()
+    order = torch.sort(key, stable=True).indices
+    last = int((key < E).sum())
+    places = torch.empty_like(order)
+    places[order] = torch.arange(order.numel())
+    places[key == E] = -1
+    order[last:] = -1
+    offsets = torch.searchsorted(key.sort().values, torch.arange(E + 1))
+    for _ in range(2):
+        got = lm.llmint8_expert_plan(ids, E)
+        assert torch.equal(got.offsets.cpu().long(), offsets)
+        assert torch.equal(got.order.cpu().long(), order)
+        assert torch.equal(got.places.cpu().long(), places.view(M, k))
+
+
 @pytest.mark.parametrize("M,K,N", FP8)
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_fp8_variants(lm, M, K, N, dtype):

@@ -35,7 +35,9 @@ class Rows(C.Structure):
     _fields_ = [("offsets", p), ("order", p), ("places", p), ("E", i64), ("k", i64)]
 L.llmint8_route.argtypes = [p, i64, i64, i64, i, i64, p, p, p, p]
 L.llmint8_route_backward.argtypes = [p, p, i64, i64, i64, i, i64, p, p, p, i64, p]
-L.llmint8_expert_plan.argtypes = [p, i64, i64, i64, p, p, p, p]
+L.llmint8_expert_plan.argtypes = [p, i64, i64, i64, p, p, p, p, sz, p]
+L.llmint8_expert_plan_workspace_size.argtypes = [i64] * 3
+L.llmint8_expert_plan_workspace_size.restype = sz
 L.llmint8_experts_gated.argtypes = [p, i64, i64, i64, p, p, i64, i64, i64, p, p, i, i, p, i64, p, p,
                                     i64, p, sz, p]
 L.llmint8_experts_gated_backward.argtypes = [p, i64, i64, i64, p, i64, i64, p, p, i64, i64, p, p,
@@ -61,8 +63,8 @@ def route(name, x=A, M=4, E=16, ld=16, dt=0, k=2, ids=B, w=B, **o):
 def rback(name, d=A, x=A, M=4, E=16, ld=16, dt=0, k=2, ids=A, dx=B, ldd=16, **o):
     res["rb_" + name] = L.llmint8_route_backward(d, x, M, E, ld, dt, k, ids, C.byref(opts(**o)), dx,
                                                  ldd, None)
-def plan(name, ids=A, M=4, k=2, E=16, offsets=B, order=B, places=B):
-    res["p_" + name] = L.llmint8_expert_plan(ids, M, k, E, offsets, order, places, None)
+def plan(name, ids=A, M=4, k=2, E=16, offsets=B, order=B, places=B, ws=A, wsb=BIG):
+    res["p_" + name] = L.llmint8_expert_plan(ids, M, k, E, offsets, order, places, ws, wsb, None)
 def rows(E=4, k=2, offsets=A, order=A, places=A):
     return Rows(offsets, order, places, E, k)
 def ref(r):
@@ -113,6 +115,7 @@ plan("null_places", places=N0); plan("M0", M=0); plan("k0", k=0); plan("k65", k=
 plan("k_over_E", k=17); plan("E0", E=0); plan("E_large", E=1025); plan("pairs", M=1 << 24)
 plan("mis_ids", ids=MIS); plan("odd_order", order=A + 2); plan("odd_places", places=A + 1)
 plan("odd_offsets", offsets=A + 3); plan("k_huge", k=1 << 62, M=8)
+plan("ws_null", M=70000, ws=N0); plan("ws_small", M=70000, wsb=64); plan("ws_mis", M=70000, ws=MIS)
 def plan_faults(f):
     f("no_plan", r=None); f("E0", r=rows(E=0)); f("E_large", r=rows(E=1025)); f("k0", r=rows(k=0))
     f("k_over_E", r=rows(k=5)); f("null_offsets", r=rows(offsets=N0))
@@ -162,6 +165,8 @@ q["matmul_back"] = W("matmul_backward", 300, 64, 128, 4, 2)
 q["bad"] = [W(n, *a) for n in ("gated", "gated_backward", "matmul", "matmul_backward")
             for a in ((0, 64, 64, 4, 2), (4, 60, 64, 4, 2), (4, 64, 64, 4, 5), (4, 64, 64, 1025, 5),
                       (1 << 24, 64, 64, 4, 2), (4, 64, -64, 4, 2))]
+P = L.llmint8_expert_plan_workspace_size
+q["plan"] = [P(1, 8, 64), P(8192, 8, 256), P(1 << 21, 8, 256), P(2048, 8, 256), P(70000, 2, 1025), P(1 << 24, 2, 8)]
 F = L.llmint8_linear_blockwise_fp8_workspace_size
 q["fp8"] = [F(1, 4096, 4096), F(300, 4096, 4096), F(1, 24, 64), F(0, 64, 64), F(4, 131088, 64)]
 print(json.dumps([res, q]))
@@ -184,11 +189,11 @@ qx_null_q qx_null_s qx_M0 qx_K0 qx_lds qx_lds_huge qx_ldx qx_dt f_null_X f_null_
 f_M0 f_N0 f_K0 f_K_large f_lds f_ldx f_ldy f_dt""".split()
 UNSUPPORTED = [f"{c}_{n}" for c in ("g", "gb", "m", "mb") for n in PLAN_UNSUPPORTED] + """
 r_odd_x r_odd_x32 r_odd_ids r_odd_w r_odd_bias rb_odd_dx rb_odd_dx32 rb_odd_d p_mis_ids p_odd_order
-p_odd_places p_odd_offsets g_mis_X g_mis_H g_mis_G g_odd_w g_ldx_mis g_span gb_mis_dX gb_mis_dWg
+p_odd_places p_odd_offsets p_ws_mis g_mis_X g_mis_H g_mis_G g_odd_w g_ldx_mis g_span gb_mis_dX gb_mis_dWg
 gb_odd_dw m_mis_R m_mis_Y mb_mis_dH mb_mis_dWd qw_K24 qw_N60 qw_mis_W qw_mis_q qx_K24 qx_mis_X
 qx_mis_q f_K24 f_N60 f_mis_X f_mis_q f_mis_b f_mis_Y f_ws_mis f_M_huge""".split()
 WORKSPACE = """g_ws_small g_ws_null gb_ws_null gb_ws_small m_ws_null m_ws_small mb_ws_null
-mb_ws_small f_ws_null f_ws_small""".split()
+mb_ws_small p_ws_null p_ws_small f_ws_null f_ws_small""".split()
 
 
 def test_refusals_before_any_hip_call():
@@ -208,6 +213,8 @@ def test_refusals_before_any_hip_call():
     assert q["gated_back"] >= 600 * (2 * 128 * 2 + 64 * 2 + 64 * 4)
     assert q["matmul"] >= 6000 * 64 * 2 and q["matmul_back"] >= 600 * 64 * 2
     assert not any(q["bad"])
+    # counts of 64 and of 256 chunks
+    assert q["plan"] == [0, 64 * 257 * 4, 256 * 257 * 4, 0, 0, 0]
     assert q["fp8"][0] == 0 and q["fp8"][1] >= 300 * 4096 and not any(q["fp8"][2:])
 
 
