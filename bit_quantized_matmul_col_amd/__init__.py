@@ -1,4 +1,5 @@
-"""MI355X (gfx950) LLM.int8() mixed-precision linear layer.
+"""MI355X (gfx950) LLM.int8() mixed-precision linear layer, the 16-bit feed-forward layers
+beside it (dense and routed to experts, forward and backward) and their FP8 forms.
 
 Thin ctypes binding over libllmint8.so (include/llmint8.h). The Python
 functions carry the C entry points' names and do argument marshalling only:

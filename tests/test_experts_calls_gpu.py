@@ -492,3 +492,37 @@ def test_block_scaled_weights_past_2_31(lm, M):
         want, tol = bo.linear(x, codes, sw[b0:-(-n1 // 128)], None, BF16)
         near(y[:, n0:n1], (want[:, n0 - b0 * 128:], tol[:, n0 - b0 * 128:]))
     torch.cuda.empty_cache()
+
+
+def test_training_example():
+    """The example runs, and its gradients are those of 64 bits with the choice held."""
+    say("training example")
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "train_routed_feed_forward.py")
+    spec = importlib.util.spec_from_file_location("train_routed_feed_forward", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    losses, W, bias = ex.train(steps=3, tokens=100, width=64, hidden=40, experts=8, k=2, dtype=F16)
+    assert len(losses) == 3 and all(math.isfinite(v) for v in losses)
+    g = gen(9)
+    X, D = rand(g, 60, 64, F16), rand(g, 60, 64, F16, 0.1)
+    Y, saved = ex.forward(X, W, 2, bias, keep=True)
+    assert torch.equal(Y, ex.forward(X, W, 2, bias)[0])
+    grads, dX = ex.backward(D, W, saved)
+    ids = saved[2].long()
+    x, *w = [t.detach().double().cpu().requires_grad_() for t in (X, *W)]
+    s = torch.sigmoid(torch.gather(x @ w[0], 1, ids.cpu()))
+    s = s / s.sum(1, keepdim=True)
+    y = x
+    for e in range(8):
+        h = fo.act("silu", x @ w[1][e]) * (x @ w[2][e])
+        y = y + (s * (ids.cpu() == e)).sum(1, keepdim=True) * (h @ w[3][e])
+    (y * D.double().cpu()).sum().backward()
+    # independent roundings of 2^-11, a dozen at most one after the other (logits, G, U, H, dH,
+    # dG, dU, dlogits and the results), of which the logits' is multiplied by what w (1 - s) and
+    # the gradients' cancellation over the chosen make of it: a hundredth of the norm
+    for name, got, want in zip(("dX", "dWr", "dWg", "dWu", "dWd"), (dX, *grads), (x, *w)):
+        got, want = got.double().cpu(), want.grad
+        assert float((got - want).norm()) <= 0.01 * float(want.norm()), name
