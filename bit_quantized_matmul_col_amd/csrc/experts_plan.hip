@@ -8,7 +8,8 @@
 // MI355X (bf16, graph replay; 8 to 128 experts, 512 x 512 to 4096 x 11008, 1 to 400 rows an
 // expert, unevenly spread): the plans chosen by them cost 3.7 % more than the best candidate
 // (geometric mean over 224 products, at worst 48 %, where the spread makes one more round of
-// 256-tiles than the mean does). Some of the choices, in microseconds:
+// 256-tiles than the mean does; on 84 products not fitted to, whose weights came from HBM, 2.1 %).
+// Some of the choices, in microseconds:
 //   2 of 16, 1 token, 4096 x 2048, gated             16 rows by 64 columns in 4 parts 20, whole 22
 //   8 of 128, 8 tokens, 768 x 2048, second product   16 rows by 64 columns 25.4, by 128 26.1
 //   8 of 128, 192 tokens, the same                   128-tiles 39, few rows 50

@@ -60,6 +60,30 @@ def test_plans_of_many_pairs(lm, M, k, E):
         assert torch.equal(got.places.cpu().long(), places.view(M, k))
 
 
+@pytest.mark.parametrize("E,k,groups,top,best", [(256, 8, 8, 4, 2), (256, 8, 1, 1, 1), (64, 6, 4, 2, 1),
+                                                 (512, 16, 16, 5, 2), (1000, 3, 1, 1, 1)])
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+def test_choices_between_close_values(lm, E, k, groups, top, best, scores):
+    """Scores with a bias that differ by fractions of what fp32 can tell: the choice is that of 64
+    bits. Rows of logits a few units of their last place apart, whose biases make up for most
+    of it; tiny scores beside a bias of 1; ties; and rows with one clear order."""
+    say("close values", E, k, groups, scores)
+    g = gen(E + k)
+    M = 96
+    base = torch.randn((M, 1), generator=g, device="cuda")
+    x = base + torch.randint(-3, 4, (M, E), generator=g, device="cuda") * 2.0 ** -22
+    x[24:48] = torch.randn((24, E), generator=g, device="cuda") - 60
+    x[48:60] = torch.randn((12, E), generator=g, device="cuda") * 3
+    x[60:72, ::2] = x[60:72, 1::2]
+    x[72:84] = torch.randn((12, E), generator=g, device="cuda").to(BF16).float()
+    bias = torch.randint(-2, 3, (E,), generator=g, device="cuda") * 2.0 ** -26
+    for b in (bias, bias + 1, torch.zeros_like(bias)):
+        kw = dict(scores=scores, bias=b, groups=groups, top_groups=top, group_best=best)
+        ids, w = lm.llmint8_route(x, k, **kw)
+        assert torch.equal(ids, eo.choose(x, k, scores, b, groups, top, best))
+        near(w, eo.mix(x, ids, scores, False))
+
+
 @pytest.mark.parametrize("M,K,N", FP8)
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_fp8_variants(lm, M, K, N, dtype):
@@ -367,6 +391,24 @@ def test_not_finite(lm, M, K, N, E, k):
         assert torch.equal(a[0][keep], b[0][keep])
         others = [x for x in range(E) if x not in s.ids[i].tolist()]
         assert torch.equal(a[1][others], b[1][others])
+
+
+@pytest.mark.parametrize("name", fo.ACTS)
+def test_every_activation(lm, name):
+    """Few rows, in one part and in several, and tiles; forward and backward."""
+    say("activation", name)
+    for M, K, N, E, k in ((1, 4096, 136, 3, 2), (60, 264, 136, 6, 2), (3000, 136, 264, 5, 2)):
+        s = Experts(lm, M, K, N, E, k, 0.0, BF16)
+        h = lm.llmint8_experts_gated(s.X, s.Wg, s.Wu, s.plan, weights=s.w, activation=name)
+        near(h, eo.gated(s.X.double(), s.Wg.double(), s.Wu.double(), s.p, s.w, name, BF16)["H"])
+        got = lm.llmint8_experts_gated_backward(s.dH, s.X, s.Wg, s.Wu, s.G, s.U, s.plan,
+                                                weights=s.w, activation=name)
+        want = eo.gated_backward(s.dH.double(), s.X.double(), s.Wg.double(), s.Wu.double(),
+                                 s.G.double(), s.U.double(), s.p, s.w, name, BF16)
+        for t, n in zip(got, ("dX", "dWg", "dWu", "dw")):
+            near(t, want[n])
+    with pytest.raises(ValueError):
+        lm.llmint8_experts_gated(s.X, s.Wg, s.Wu, s.plan, activation="swish")
 
 
 def test_broadcast_weights(lm):
