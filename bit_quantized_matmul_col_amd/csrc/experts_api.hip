@@ -193,7 +193,7 @@ LLMINT8_EXPORT int llmint8_expert_plan(const int32_t *ids, int64_t M, int64_t k,
   Check c;
   check_rows(c, M, 8, 8, E, k);
   c.need(ids && offsets && order && places);
-  c.want(aligned16(ids) && aligned4(offsets) && aligned4(order) && aligned4(places));
+  c.want(aligned4(ids) && aligned4(offsets) && aligned4(order) && aligned4(places));
   if (const int st = c.status()) return st;
   const size_t need = expert_plan_scratch(M * k, (int)E);
   if (const int st = check_workspace(workspace, workspace_bytes, need)) return st;

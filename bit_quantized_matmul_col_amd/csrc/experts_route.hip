@@ -328,8 +328,9 @@ __global__ __launch_bounds__(kPlanThreads) void k_expert_plan(const int32_t *ids
   // wave wv has the pairs p0 .. p1 - 1, in steps of 256: 4 of a lane
   const int64_t step = (pairs + 256 * kPlanWaves - 1) / (256 * kPlanWaves) * 256;
   const int64_t p0 = wv * step, p1 = p0 + step < pairs ? p0 + step : pairs;
+  const bool whole = ((uintptr_t)ids & 15u) == 0;  // four ids a load
   auto load = [&](int64_t p, int *id) {
-    if (p + 4 <= p1) {
+    if (whole && p + 4 <= p1) {
       const i32x4 v = *(const i32x4 *)(ids + p);
 #pragma unroll
       for (int q = 0; q < 4; ++q) id[q] = (uint32_t)v[q] < (uint32_t)E ? v[q] : E;

@@ -456,6 +456,7 @@ int llmint8_route_backward(const float *dweights, const void *logits, int64_t M,
  *   offsets  [E + 1]: expert e has the rows offsets[e] .. offsets[e + 1] - 1.
  *   order    [M k]: the pair of each row, an expert's pairs in rising order; -1 behind the last.
  *   places   [M x k]: the row of each pair, -1 for an id outside 0 .. E - 1, which has none.
+ * The ids, the plan and the weights need their type's alignment alone.
  * llmint8_expert_plan fills the three from ids [M x k]; nothing depends on the order in which
  * blocks run. Its workspace has llmint8_expert_plan_workspace_size bytes (may be 0: NULL then).
  * The calls below take them in an llmint8_expert_rows, and check what they read from

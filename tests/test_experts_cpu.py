@@ -113,7 +113,7 @@ rback("odd_d", d=A + 2); rback("struct", size=0)
 plan("null_ids", ids=N0); plan("null_offsets", offsets=N0); plan("null_order", order=N0)
 plan("null_places", places=N0); plan("M0", M=0); plan("k0", k=0); plan("k65", k=65, E=100)
 plan("k_over_E", k=17); plan("E0", E=0); plan("E_large", E=1025); plan("pairs", M=1 << 24)
-plan("mis_ids", ids=MIS); plan("odd_order", order=A + 2); plan("odd_places", places=A + 1)
+plan("odd_ids", ids=A + 2); plan("odd_order", order=A + 2); plan("odd_places", places=A + 1)
 plan("odd_offsets", offsets=A + 3); plan("k_huge", k=1 << 62, M=8)
 plan("ws_null", M=70000, ws=N0); plan("ws_small", M=70000, wsb=64); plan("ws_mis", M=70000, ws=MIS)
 def plan_faults(f):
@@ -188,7 +188,7 @@ mb_lddw mb_sdw_overlap qw_null_W qw_null_q qw_null_s qw_K0 qw_N0 qw_K_large qw_l
 qx_null_q qx_null_s qx_M0 qx_K0 qx_lds qx_lds_huge qx_ldx qx_dt f_null_X f_null_q f_null_s f_null_Y
 f_M0 f_N0 f_K0 f_K_large f_lds f_ldx f_ldy f_dt""".split()
 UNSUPPORTED = [f"{c}_{n}" for c in ("g", "gb", "m", "mb") for n in PLAN_UNSUPPORTED] + """
-r_odd_x r_odd_x32 r_odd_ids r_odd_w r_odd_bias rb_odd_dx rb_odd_dx32 rb_odd_d p_mis_ids p_odd_order
+r_odd_x r_odd_x32 r_odd_ids r_odd_w r_odd_bias rb_odd_dx rb_odd_dx32 rb_odd_d p_odd_ids p_odd_order
 p_odd_places p_odd_offsets p_ws_mis g_mis_X g_mis_H g_mis_G g_odd_w g_ldx_mis g_span gb_mis_dX gb_mis_dWg
 gb_odd_dw m_mis_R m_mis_Y mb_mis_dH mb_mis_dWd qw_K24 qw_N60 qw_mis_W qw_mis_q qx_K24 qx_mis_X
 qx_mis_q f_K24 f_N60 f_mis_X f_mis_q f_mis_b f_mis_Y f_ws_mis f_M_huge""".split()
