@@ -971,8 +971,8 @@ def llmint8_route(logits: torch.Tensor, k: int, *, scores: str = "softmax",
     if groups < 1 or E % groups:
         raise ValueError(f"groups must divide the {E} experts, got {groups}")
     opts = _route_opts(logits, scores, bias, groups, top_groups, group_best, renormalize, scale)
-    ids = torch.empty((M, k), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((M, k), dtype=torch.float32, device=logits.device)
+    ids = logits.new_empty((M, k), dtype=torch.int32)
+    weights = logits.new_empty((M, k), dtype=torch.float32)
     _launch(lib().llmint8_route, logits, logits.data_ptr(), M, E, ld, _LOGIT_TYPES[logits.dtype],
             k, opts, ids.data_ptr(), weights.data_ptr())
     return ids, weights
@@ -1009,7 +1009,7 @@ def llmint8_expert_plan(ids: torch.Tensor, experts: int) -> ExpertPlan:
     need = lib().llmint8_expert_plan_workspace_size(M, k, experts)
     # one allocation: the parts, the workspace first, begin at multiples of 16 bytes
     w, a, b = (need + 15) // 16 * 4, (experts + 4) // 4 * 4, (M * k + 3) // 4 * 4
-    held = torch.empty((w + a + 2 * b,), dtype=torch.int32, device=ids.device)
+    held = ids.new_empty((w + a + 2 * b,))
     plan = ExpertPlan(held.as_strided((experts + 1,), (1,), w),
                       held.as_strided((M * k,), (1,), w + a),
                       held.as_strided((M, k), (k, 1), w + a + b))

@@ -413,7 +413,8 @@ int llmint8_gated_backward(const uint16_t *dH, int64_t M, int64_t N, int64_t ldd
 /*
  * Routed feed-forward layers: a router sends each of M tokens to k of E experts, each a gated
  * block with weights of its own. Rules as for the 16-bit operators above; E is at most 1024, k
- * at most E and at most 64, M k below 2^25.
+ * at most E and at most 64, M k below 2^25. (A product of more than 2^24 blocks of 16 rows by 64
+ * columns for few rows an expert, or of more than 2^30 tiles of 128 x 128, is UNSUPPORTED.)
  *
  * llmint8_route: the experts of each token and their weights, from the router's logits.
  *   logits   [M x E], leading dimension ld >= E, of `dtype` LLMINT8_FP16, _BF16 or _FP32 (no
