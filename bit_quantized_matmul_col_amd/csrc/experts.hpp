@@ -49,8 +49,8 @@ FfnPlan experts_plan(FfnKind kind, int64_t pairs, int E, int64_t N, int64_t K);
 
 // Products over the rows of each expert: `a` for all rows (a.M = the number of pairs, a.b and
 // a.pairs those of expert 0 and row 0); expert e's B is bstride elements after the last's.
-// Forward and GradX: rows as they are, sums to a.y, or to a.part in fp32. Gated: rows of the
-// tokens, or as they are.
+// Forward: rows as they are, sums to a.part in fp32. GradX: the same, or to a.y in 16 bits. Gated: rows
+// of the tokens, or as they are.
 hipError_t launch_expert_rows(FfnKind kind, int dtype, const FfnGemm &a, const Pairs &p,
                               int64_t bstride, const FfnPlan &plan, hipStream_t s);
 hipError_t launch_expert_skinny(int dtype, bool gated, const FfnGemm &a, const Pairs &p,
@@ -63,10 +63,9 @@ hipError_t launch_expert_grad_w(int dtype, const FfnGemm &a, const Pairs &p, int
 // out[r] = x[token of row r]
 hipError_t launch_take_rows(int dtype, const uint16_t *x, int64_t ldx, int64_t cols,
                             const Pairs &p, uint16_t *out, hipStream_t s);
-// y[i] = residual[i] + the sum over token i's pairs of their rows: 16-bit rows [rows x N], or
-// `parts` planes of fp32 ones.
+// y[i] = residual[i] + the sum over token i's pairs of their rows, `parts` planes of fp32
+// [rows x N].
 struct Combine {
-  const uint16_t *rows;
   const float *part;
   int parts;
   int64_t N;

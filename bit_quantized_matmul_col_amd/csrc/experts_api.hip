@@ -111,7 +111,7 @@ GatedLayout gated_layout(int64_t M, int64_t K, int64_t N, int64_t E, int64_t k) 
   return L;
 }
 
-// The second product's rows before they are summed: fp32 parts of the few-row kernel, or 16 bits.
+// The second product's rows before they are summed, in fp32, in the plan's parts.
 struct MatmulLayout {
   size_t total;
   FfnPlan plan;
@@ -119,7 +119,7 @@ struct MatmulLayout {
 MatmulLayout matmul_layout(int64_t M, int64_t K, int64_t N, int64_t E, int64_t k) {
   MatmulLayout L{};
   L.plan = experts_plan(FfnKind::Forward, M * k, (int)E, K, N);
-  L.total = up(L.plan.few ? part_bytes(L.plan, M * k, K, 1) : (size_t)M * k * K * 2);
+  L.total = up(part_bytes(L.plan, M * k, K, 1));
   return L;
 }
 
@@ -306,7 +306,7 @@ LLMINT8_EXPORT int llmint8_experts_gated_backward(
     const FfnPlan plan = experts_plan(FfnKind::GradX, p.rows(), p.E, K, 2 * N);
     e = launch_expert_rows(FfnKind::GradX, dtype, a, p, stride_w, plan, s);
     if (e == hipSuccess)
-      e = launch_combine(dtype, Combine{nullptr, xrows, 1, K, nullptr, 0, dX, lddx}, p, s);
+      e = launch_combine(dtype, Combine{xrows, 1, K, nullptr, 0, dX, lddx}, p, s);
   }
   if (e == hipSuccess && dWg) {
     e = launch_take_rows(dtype, X, ldx, K, p, xs, s);
@@ -342,12 +342,11 @@ LLMINT8_EXPORT int llmint8_experts_matmul(const uint16_t *H, int64_t M, int64_t 
   if (const int st = check_workspace(workspace, workspace_bytes, L.total)) return st;
   hipStream_t s = (hipStream_t)stream;
   const Pairs p = pairs_of(rows, M);
-  FfnGemm a = rows_gemm(H, ldh, Wd, ldw, K, N, p, (uint16_t *)workspace, K);
-  if (L.plan.few)
-    a.part = (float *)workspace, a.ksplit = L.plan.ksplit, a.to_parts = 1;
+  FfnGemm a = rows_gemm(H, ldh, Wd, ldw, K, N, p, nullptr, 0);
+  a.part = (float *)workspace, a.ksplit = L.plan.ksplit, a.to_parts = 1;
   hipError_t e = launch_expert_rows(FfnKind::Forward, dtype, a, p, stride_w, L.plan, s);
   if (e == hipSuccess)
-    e = launch_combine(dtype, Combine{a.y[0], a.part, a.ksplit, K, residual, ldr, Y, ldy}, p, s);
+    e = launch_combine(dtype, Combine{a.part, a.ksplit, K, residual, ldr, Y, ldy}, p, s);
   return hip_status(e);
 }
 

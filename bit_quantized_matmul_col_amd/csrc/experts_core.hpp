@@ -262,8 +262,10 @@ __device__ __forceinline__ void run_tiles(int64_t lda, int64_t ldb, int nsegs, u
     cur = ld.out, left = nst;
     active = wm * C::WM < cur.rows && wn * C::WO < cur.cols;
   };
-  // whether the sums go to `part` in fp32
-  const bool wide = C::LA == Lay::RowK && kernel_args<K>()->a.to_parts;
+  // whether the rows go to `part` in fp32: the second product's always (a token's are still to be
+  // summed, and rounded then), of the gradients by rows dX's
+  const bool wide =
+      C::LA == Lay::RowK && (C::LB == Lay::ColK || kernel_args<K>()->a.to_parts);
   auto store_tile = [&]() {
     // computed here, not kept in registers beside the loop's
     int lane = threadIdx.x & 63;

@@ -24,11 +24,11 @@ __global__ __launch_bounds__(kThreads) void k_take_rows(const uint16_t *x, int64
   });
 }
 
-// The rows of a token's pairs are summed in fp32, in the order of its choices. The second product's
-// tiles leave them in 16 bits: each was rounded once, as the sum will be, and fp32 would be twice
-// the bytes of the largest pass next to the product. dX's come in fp32, since they were summed from
-// operands that had been rounded already.
-template <class T, bool F32>
+// The rows of a token's pairs come in fp32, the second product's and dX's alike, and are summed in the
+// order of its choices; the sum is rounded once. Rows in 16 bits would be half the bytes (the second
+// product of 4096 tokens x 4 of 32 experts, 2048 x 4096: 339 us instead of 397), but they may cancel,
+// or lie beyond fp16's range, where their sum does not.
+template <class T>
 __global__ __launch_bounds__(kThreads) void k_combine(Combine c, Pairs p, int cx_log2) {
   const int64_t rows = p.rows();
   for_rows(cx_log2, p.tokens, c.N, [&](int64_t i, int64_t n, bool in) {
@@ -43,13 +43,9 @@ __global__ __launch_bounds__(kThreads) void k_combine(Combine c, Pairs p, int cx
         const int64_t r = j0 + q < p.k ? p.places[i * p.k + j0 + q] : -1;
         has[q] = r >= 0 && r < rows;
         if (!has[q]) continue;
-        if constexpr (F32) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[q][e] = 0.f;
-          join_parts(c.part + r * c.N + n, rows * c.N, c.parts, x[q]);
-        } else {
-          load8<T>(c.rows + r * c.N + n, x[q]);
-        }
+        for (int e = 0; e < 8; ++e) x[q][e] = 0.f;
+        join_parts(c.part + r * c.N + n, rows * c.N, c.parts, x[q]);
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -128,8 +124,7 @@ hipError_t launch_take_rows(int, const uint16_t *x, int64_t ldx, int64_t cols, c
 
 hipError_t launch_combine(int dtype, const Combine &c, const Pairs &p, hipStream_t s) {
   const RowGrid g = row_grid(p.tokens, c.N, kMaxGridY);
-  auto *kern = dtype == LLMINT8_FP16 ? (c.part ? k_combine<Half, true> : k_combine<Half, false>)
-                                     : (c.part ? k_combine<Bfloat, true> : k_combine<Bfloat, false>);
+  auto *kern = dtype == LLMINT8_FP16 ? k_combine<Half> : k_combine<Bfloat>;
   hipLaunchKernelGGL(kern, g.grid, dim3(kThreads), 0, s, c, p, g.cx_log2);
   return hipGetLastError();
 }

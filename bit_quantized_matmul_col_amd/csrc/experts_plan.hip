@@ -12,10 +12,12 @@
 // Some of the choices, in microseconds:
 //   2 of 16, 1 token, 4096 x 2048, gated             16 rows by 64 columns in 4 parts 20, whole 22
 //   8 of 128, 8 tokens, 768 x 2048, second product   16 rows by 64 columns 25.4, by 128 26.1
-//   8 of 128, 192 tokens, the same                   128-tiles 39, few rows 50
+//   8 of 128, 192 tokens, the same                   128-tiles 46, few rows 53
 //   2 of 8, 160 tokens, 11008 x 4096, the same       64 rows by 128 in 2 parts 153, whole 180
 //   4 of 32, 720 tokens, 2048 x 1024, gated          256-tiles 63, 128-tiles 75, few rows 84
 //   8 of 32, 1600 tokens, 7168 x 2048, gated         256-tiles 872, 128-tiles 985
+// The second product's tiles were timed with rows in 16 bits then; with rows in fp32 (88 products
+// timed again) the same constants choose within 3.1 % of the best, refitted ones within 3.9 %.
 // The plan is a function of the shape alone, so that the workspace query and the call agree.
 #include "experts.hpp"
 

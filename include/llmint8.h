@@ -516,9 +516,8 @@ int llmint8_experts_gated_backward(const uint16_t *dH, int64_t M, int64_t N, int
 /*
  * The experts' second product and the sum over each token's experts:
  *   Y[i] = R[i] + sum over token i's rows r of H[r] . Wd_e,
- * H [M k x N] in the plan's order, Wd [E][N x K], R and Y [M x K] (R may be NULL). The rows are
- * summed in fp32 in the order of the token's choices; where experts have many rows, each
- * product is rounded to 16 bits before.
+ * H [M k x N] in the plan's order, Wd [E][N x K], R and Y [M x K] (R may be NULL). The rows stay in
+ * fp32 and are summed in the order of the token's choices; the sum is rounded once.
  * Gradients: dH[r] = dY[i] . Wd_e^T (rows behind the plan's last left as they were), dWd_e =
  * H_e^T . dY_e; either may be NULL. R's gradient is dY itself.
  */
