@@ -146,7 +146,7 @@ __device__ __forceinline__ void run_tiles(int64_t lda, int64_t ldb, int nsegs, u
   TB B;
   int n1, nst, ls, lpar = 0;  // its stages a segment and in all, the next to load, its parity
   bool more = true;
-  // the pairs of a tile's rows to LDS; -1 past them
+  // the pairs of a tile's rows to LDS; past them 0, which is not used
   auto bring_pairs = [&](const Job &j, int par, int lane) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(j.pairs, j.out.rows * 4),
                                              (lptr_t)(prow + par * BM + row64), 4,
@@ -356,7 +356,8 @@ __device__ __forceinline__ void run_tiles(int64_t lda, int64_t ldb, int nsegs, u
   if constexpr (C::ROUTED) {
     find(kernel_args<K>(), tile, ld);
     bring_pairs(ld, 0, lane);
-    __syncthreads();  // waits for the loads too
+    wait_vm<0>();  // the other waves read them behind the barrier
+    __syncthreads();
   }
   begin();
   Loads l = next();
