@@ -168,7 +168,11 @@ __global__ __launch_bounds__(64 * kRows) void k_route(Route r, int32_t *ids, flo
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (lane + 64 * v < r.E) mine[lane + 64 * v] = key[v] ? val[v] : kNone;
+    // the lanes read what others wrote: no instruction, since a wave's LDS accesses are in order,
+    // but the compiler has to keep them so
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     Value best = kNone, second = kNone;
     const int group = lane / per;
     if (group < r.groups)

@@ -43,3 +43,16 @@ def test_the_first_pairs_of_a_tile_have_arrived_before_other_waves_read_them(tmp
         assert "wait_vmILi0E" in calls[barriers[0] - 1], calls[:barriers[0] + 1]
         seen += 1
     assert seen == 4  # two types, two tiles
+
+
+def test_group_values_pass_between_lanes_in_order(tmp_path):
+    """A wave writes its row's values to LDS and its lanes read each other's: release before the
+    meeting, acquire behind it (the meeting alone orders no memory)."""
+    seen = 0
+    for name, calls in functions("experts_route.hip", tmp_path).items():
+        meet = [i for i, c in enumerate(calls) if "@llvm.amdgcn.wave.barrier" in c]
+        for i in meet:
+            assert calls[i - 1] == 'fence syncscope("wavefront") release', (name, calls[i - 1])
+            assert calls[i + 1] == 'fence syncscope("wavefront") acquire', (name, calls[i + 1])
+            seen += 1
+    assert seen == 10  # five widths of a row, two kinds of value
