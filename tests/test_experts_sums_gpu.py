@@ -61,3 +61,24 @@ def test_second_product_of_rows_that_cancel(lm, M, K, N, E, k, dtype):
     Y.check()
     assert torch.equal(Y.t, (want + R).to(dtype))
     assert torch.equal(lm.llmint8_experts_matmul(s.rows(dtype), Wd, s.plan), want.to(dtype))
+
+
+@pytest.mark.parametrize("M,K,N,E,k", SHAPES)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_gradient_of_rows_that_cancel(lm, M, K, N, E, k, dtype):
+    """dX, likewise: without an activation, with G = 1, U = 2 and weights of a half, dG = dH and
+    dU = dH / 2 are whole numbers of 16 bits, so that nothing rounds but the sum."""
+    say("gradient rows that cancel", M, K, N, E, k, dtype)
+    s = Cancelling(lm, M, N, E, k, 1)
+    Bg, Bu = whole(s.g, 1, 5, K, N), whole(s.g, 1, 9, K, N)
+    both = (2 * Bg + Bu).t()
+    row = s.v[:, 0] @ both
+    assert float(row.max()) > 65504 and 2 * float(row.max()) < 2 ** 24
+    Wg, Wu = (t.to(dtype).expand(E, -1, -1).contiguous() for t in (Bg, Bu))
+    one = torch.ones((M * k, N), dtype=dtype, device="cuda")
+    half = torch.full((M, k), 0.5, device="cuda")
+    dX = Band(M, K, dtype)
+    lm.llmint8_experts_gated_backward(s.rows(dtype, 2), None, Wg, Wu, one, 2 * one, s.plan,
+                                      weights=half, activation="none", dX=dX.t, need_dW=False)
+    dX.check()
+    assert torch.equal(dX.t, (s.v.sum(1) @ both).to(dtype))
