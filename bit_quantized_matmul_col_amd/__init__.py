@@ -962,8 +962,8 @@ def llmint8_route(logits: torch.Tensor, k: int, *, scores: str = "softmax",
     are chosen, ties to the lower index, in falling order; with groups > 1 out of the top_groups
     best of `groups` equal runs of experts, a run's value being the sum of its group_best (1 or 2)
     largest. weights are the scores of the chosen, divided by their sum with `renormalize`, times
-    `scale`. An expert whose logit is -inf or NaN is out: where fewer than k are left, the id is
-    -1 and the weight 0."""
+    `scale`. An expert whose logit is -inf or NaN is out, and one whose bias is: where fewer than k
+    are left, the id is -1 and the weight 0."""
     ld = _logits(logits)
     M, E = logits.shape
     if not 1 <= k <= min(E, 64):
@@ -999,7 +999,9 @@ def llmint8_route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: to
 
 def llmint8_expert_plan(ids: torch.Tensor, experts: int) -> ExpertPlan:
     """The experts' order of the pairs that ids int32 [M, k] name (ids outside 0 .. experts - 1:
-    none). It serves every call on these ids, the backward ones too."""
+    none, as on a rank that holds some of the experts). `experts` is at least k: a rank with fewer
+    passes k and repeats an expert's weights (W.expand) for those that no id names. The plan
+    serves every call on these ids, the backward ones too."""
     _need(ids, "ids", torch.int32, 2)
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")

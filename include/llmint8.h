@@ -421,7 +421,8 @@ int llmint8_gated_backward(const uint16_t *dH, int64_t M, int64_t N, int64_t ldd
  *            alignment beyond the type's).
  *   An expert whose logit is -infinity or NaN is out for that token: never chosen, and nothing
  *   to a softmax's sum (a padded row holds -infinity throughout). +infinity counts as the largest
- *   fp32 value. Scores: softmax over the row, or the logistic function of each logit.
+ *   fp32 value. An expert whose bias is -infinity or NaN is never chosen and adds nothing to a run's
+ *   value; its score stays part of a softmax's sum. Scores: softmax over the row, or the logistic function of each logit.
  *   Choice: the k largest of score + bias, ties to the lower index, in falling order. With
  *   groups > 1 the experts are `groups` equal runs; a run's value is the sum of its group_best
  *   (1 or 2) largest score + bias, and only the top_groups best runs take part. The order is
@@ -458,6 +459,9 @@ int llmint8_route_backward(const float *dweights, const void *logits, int64_t M,
  *   order    [M k]: the pair of each row, an expert's pairs in rising order; -1 behind the last.
  *   places   [M x k]: the row of each pair, -1 for an id outside 0 .. E - 1, which has none.
  * The ids, the plan and the weights need their type's alignment alone.
+ * A rank that holds some of the experts gives its own the numbers 0, 1, ... and all others an id
+ * outside 0 .. E - 1; one that holds fewer than k passes E = k: experts without pairs have no rows,
+ * and stride_w = 0 lets them share an expert's weights (their gradients are zeros).
  * llmint8_expert_plan fills the three from ids [M x k]; nothing depends on the order in which
  * blocks run. Its workspace has llmint8_expert_plan_workspace_size bytes (may be 0: NULL then).
  * The calls below take them in an llmint8_expert_rows, and check what they read from
@@ -494,7 +498,8 @@ int llmint8_experts_gated(const uint16_t *X, int64_t M, int64_t K, int64_t ldx,
 
 /*
  * Gradients of llmint8_experts_gated: with d = w[pair] dH[r],
- *   dG = d * U * act'(G) and dU = d * act(G) (rounded to 16 bits, the products' operands),
+ *   dG = d * U * act'(G) and dU = d * act(G) (rounded to 16 bits, the products' operands: in fp16
+ *   one beyond 65504 becomes infinite),
  *   dX[i] = the sum over token i's rows of dG . Wg_e^T + dU . Wu_e^T (fp32, rounded once),
  *   dWg_e = X_e^T . dG_e, dWu_e = X_e^T . dU_e over expert e's rows (zeros without any),
  *   dweights[pair] = sum over n of dH[r] act(G[r]) U[r] (fp32; 0 without a row).
