@@ -7,7 +7,8 @@
 // pass and the join of the parts included. The estimates' constants were fitted to 4330
 // timed calls on MI355X (bf16, graph replay, M 1 to 4500, K 256 to 11008, N 256 to 14336; root
 // mean square 8 % off); the plans chosen by them cost 0.6 % more than the best candidate (geometric
-// mean over 400 shapes, at worst 17 %). The timings are not kept here. Some of the choices, in microseconds:
+// mean over 400 shapes, at worst 17 %). The timings are not kept here. Some of the choices, in
+// microseconds:
 //   1 x 8192 x 28672       few rows, coded in place, 64 columns 44, 32 columns 52
 //   64 x 2048 x 2048       few rows 10.8, 128-tiles in 4 parts 12.9
 //   128 x 11008 x 4096     128-tiles in 8 parts 28, whole 60; few rows 36

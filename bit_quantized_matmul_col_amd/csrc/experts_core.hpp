@@ -21,8 +21,9 @@
 //
 // Measured, 4096 tokens x 4 of 32 experts, 4096 x 2048, bf16: gated 600 us (0.92 PFLOP/s; with one
 // tile a block 633), dX 616, the pair of weight gradients 750 (the whole backward call 1465; with dX's
-// rows in 16 bits 1390, and 1870 with one tile a block); the MFMAs are busy for 0.52, 0.49 and 0.38 of the time, at a clock of
-// 1.95 GHz, since 2.4 GHz would take more power than the card has. What remains is
+// rows in 16 bits 1390, and 1870 with one tile a block); the MFMAs are busy for 0.52, 0.49 and 0.38
+// of the time, at a clock of 1.95 GHz, since 2.4 GHz would take more power than the card has. What
+// remains is
 // tiles that are not full where the router is uneven (80 tile rows for 64 tiles' worth of rows;
 // 485 us with even experts), the weights' way from HBM (454 where all experts share one's) and, for
 // weight gradients, their stores (1.07 GB; 610 without them). Stages of 32 in a ring of four were

@@ -18,8 +18,9 @@
 //   8 of 32, 1600 tokens, 7168 x 2048, gated         256-tiles 872, 128-tiles 985
 // Pairs without an expert (padding, experts of other ranks) are known on the GPU alone too and count
 // as rows, so such a call is planned for more rows than there are.
-// The timings are not kept here. The second product's tiles were timed with rows in 16 bits then; with rows in fp32 (88 products
-// timed again) the same constants choose within 3.1 % of the best, refitted ones within 3.9 %.
+// The timings are not kept here. The second product's tiles were timed with rows in 16 bits then;
+// with rows in fp32 (88 products timed again) the same constants choose within 3.1 % of the best,
+// refitted ones within 3.9 %.
 // The plan is a function of the shape alone, so that the workspace query and the call agree.
 #include "experts.hpp"
 

@@ -422,7 +422,8 @@ int llmint8_gated_backward(const uint16_t *dH, int64_t M, int64_t N, int64_t ldd
  *   An expert whose logit is -infinity or NaN is out for that token: never chosen, and nothing
  *   to a softmax's sum (a padded row holds -infinity throughout). +infinity counts as the largest
  *   fp32 value. An expert whose bias is -infinity or NaN is never chosen and adds nothing to a run's
- *   value; its score stays part of a softmax's sum. Scores: softmax over the row, or the logistic function of each logit.
+ *   value; its score stays part of a softmax's sum.
+ *   Scores: softmax over the row, or the logistic function of each logit.
  *   Choice: the k largest of score + bias, ties to the lower index, in falling order. With
  *   groups > 1 the experts are `groups` equal runs; a run's value is the sum of its group_best
  *   (1 or 2) largest score + bias, and only the top_groups best runs take part. The order is
